@@ -70,7 +70,8 @@ enum {
   ONELA_ERR_CUDA = 5,        /* a CUDA call failed (allocation, launch ...)  */
   ONELA_ERR_UNSUPPORTED = 6, /* the requested kernel cannot run this shape   */
   ONELA_ERR_SCRATCH = 7,     /* onela_decode_step_noalloc: the decode does not
-                                fit in its fixed 32 MiB device array         */
+                                fit in its fixed 32 MiB device array; other
+                                calls: the caller's scratch is too small      */
   ONELA_ERR_TIMEOUT = 8      /* a bounded wait inside a kernel ran out (bit 1
                                 of the error word): the outputs of that call
                                 are void; reported by the next call or by
@@ -444,6 +445,195 @@ ONELA_API int onela_decode_step_noalloc(const onela_config *cfg, int32_t t, int3
                                         const void *S0, const void *q, const void *k, const void *v,
                                         const float *g, const float *beta, const int32_t *parent_idx,
                                         float *o, int32_t *status, onela_stream stream);
+
+/* ------------------------------------------------------------------------
+ * Around a GDN layer: the rest of a hybrid decoder's block.
+ *
+ * Models with GDN layers interleave them with full-attention layers (the
+ * abstract's linear-attention decoding is one layer kind of such a model),
+ * and every layer sits between norms.  The four operators below are what a
+ * decode loop needs between two onela_decode_step calls of such a model:
+ * attention of the beams' new tokens over a paged key-value cache whose
+ * prompt part the beams of a request share, writing to that cache, evicting
+ * from it, and the norms around a block.
+ *
+ * They hold no handle and keep nothing between calls.  Their conventions are
+ * those above; in addition
+ *   - `scratch` is a DEVICE buffer on a 256-byte boundary, owned by the
+ *     caller and borrowed for the stream-ordered duration of the call.  Its
+ *     contents need not be kept or cleared between calls; calls that may run
+ *     at the same time (other streams, two captured graphs) need scratch of
+ *     their own.
+ *   - `status` is a DEVICE int32 or NULL.  A call ORs ONELA_STATUS_* bits
+ *     into it for what its device-side data got wrong; the caller clears it.
+ *     Nothing out of range is read or written either way.
+ *
+ * The cache.  A pool holds `pages` pages of `page` tokens, K and V in arrays
+ * of their own: [pages][H_kv][page][d] in dtype.  A row (a request's prompt, or
+ * one beam's own tokens) has a table of page numbers, int32 [row_pages]; its
+ * token at position p is token p mod page of page table[p / page].  Pages may
+ * appear in several rows that only read them. */
+enum {
+  ONELA_STATUS_PAGE = 1,   /* a page number outside [0, pages) was met: the
+                              token was left out (attention), not written
+                              (write, evict) or copied as zeros (evict)      */
+  ONELA_STATUS_LENGTH = 2  /* a length, start or count outside what its row
+                              can hold was clamped, or a write fell past it */
+};
+
+/* Attention of new tokens over the cache.  Request r has W beams (W = 1: an
+ * ordinary single-token decode), each with one new token of H_q query heads,
+ * H_q a multiple of H_kv (query head h reads key-value head h / (H_q / H_kv)).
+ * Beam w of request r attends to the request's first lengths[r] prompt
+ * positions, shared by its beams, and to the first beam_lengths[r][w] tokens
+ * of its own table (if there is a beam segment):
+ *     s_j = scale * (q . k_j),   p = softmax(s),   o = sum_j p_j v_j.
+ * With beam_page = 1 a beam's table is its ancestry row: level by level the
+ * record of its ancestor, written once and never moved (review, Summary).
+ * The new token's own k and v must be in the cache before the call
+ * (onela_cache_write).  A row with nothing to attend to gives o = 0 and
+ * lse = -inf.  Cache slots past a length are not used, whatever they hold.
+ *   R, W, H_q, H_kv   >= 1; W * H_q / H_kv <= 65536.
+ *   d                 head width, 1 .. 256.
+ *   dtype             ONELA_F32 or ONELA_BF16: of q, the pools and o.
+ *                     Products are accumulated and the softmax is taken in
+ *                     fp32 either way.
+ *   kernel            ONELA_KERNEL_AUTO; ONELA_KERNEL_SIMT (any shape) or
+ *                     ONELA_KERNEL_TC (bf16, d in {64, 128, 256}, pools and q
+ *                     rows on 16-byte boundaries) to force one.
+ *   page, pages, row_pages
+ *                     the prompt pool and the entries of a table row.
+ *   beam_page, beam_pages, beam_row_pages
+ *                     the beams' pool; all 0: no beam segment.
+ *   q_stride          elements between q's tokens (>= H_q * d): q may be a
+ *                     slice of a wider projection.
+ *   scale             > 0. */
+typedef struct {
+  int32_t R, W, H_q, H_kv, d;
+  int32_t dtype;
+  int32_t kernel;
+  int32_t page, pages, row_pages;
+  int32_t beam_page, beam_pages, beam_row_pages;
+  int32_t device;
+  int64_t q_stride;
+  float scale;
+} onela_attention_config;
+
+/*   q            [R][W][H_q][d], token r * W + w at q + (r * W + w) * q_stride.
+ *   k_pool, v_pool, table, lengths
+ *                the prompt pool, int32 [R][row_pages], int32 [R].
+ *   beam_k, beam_v, beam_table, beam_lengths
+ *                the beams' pool, int32 [R][W][beam_row_pages], int32 [R][W];
+ *                NULL without a beam segment.
+ *   mass, mass_out
+ *                fp32 [R][H_kv][row_pages * page] or NULL.  With mass_out,
+ *                the attention each prompt position drew is added up over
+ *                the beams and the query heads of its key-value head:
+ *                    mass_out[r][h][j] = mass[r][h][j] + sum p_j,
+ *                for j < lengths[r]; later entries are left as they were.
+ *                mass NULL counts as zeros; mass may equal mass_out.
+ *   o            [R][W][H_q][d] in dtype, written.
+ *   lse          fp32 [R][W][H_q] or NULL: log sum_j exp(s_j).
+ *   scratch      at least onela_paged_attention_scratch_bytes(cfg, want_mass)
+ *                bytes (want_mass: whether mass_out is given); 0 for a bad cfg.
+ * Errors: ONELA_ERR_ARG, ONELA_ERR_SCRATCH, ONELA_ERR_UNSUPPORTED (the forced
+ * kernel cannot run this shape), ONELA_ERR_CUDA. */
+ONELA_API size_t onela_paged_attention_scratch_bytes(const onela_attention_config *cfg, int32_t want_mass);
+ONELA_API int onela_paged_attention(const onela_attention_config *cfg, const void *q, const void *k_pool,
+                                    const void *v_pool, const int32_t *table, const int32_t *lengths,
+                                    const void *beam_k, const void *beam_v, const int32_t *beam_table,
+                                    const int32_t *beam_lengths, const float *mass, float *mass_out, void *o,
+                                    float *lse, void *scratch, size_t scratch_bytes, int32_t *status,
+                                    onela_stream stream);
+
+/* Write tokens to the cache: row b's token i (i < n, and i < counts[b] if
+ * counts is given) goes to position start[b] + i of table row b.
+ *   k, v      [B][n][H_kv][d] in dtype, token b * n + i at k + (b * n + i) *
+ *             k_stride (v likewise).
+ *   start     int32 [B];  counts  int32 [B] or NULL (n for every row).
+ * Tokens that fall outside the row or on a bad page are dropped and reported
+ * in status.  Two tokens of a call must not share a cache slot.
+ * Errors: ONELA_ERR_ARG, ONELA_ERR_CUDA. */
+typedef struct {
+  int32_t B, n, H_kv, d;
+  int32_t dtype;
+  int32_t page, pages, row_pages;
+  int32_t device;
+  int64_t k_stride, v_stride;
+} onela_cache_write_config;
+ONELA_API int onela_cache_write(const onela_cache_write_config *cfg, const void *k, const void *v, void *k_pool,
+                                void *v_pool, const int32_t *table, const int32_t *start, const int32_t *counts,
+                                int32_t *status, onela_stream stream);
+
+/* Evict from the cache by accumulated attention weight.  Every (request,
+ * key-value head) keeps n = min(lengths[r], keep) of its positions: the last
+ * min(recent, n), and of the ones before them those with the largest mass
+ * (ties to the smaller position; +0 and -0 are equal; NaN below every
+ * number).  The kept tokens are copied, in their order, to positions 0 .. n-1
+ * of the row's new table, with their mass; heads keep different tokens.
+ *   k_pool, v_pool, table, lengths, mass
+ *                the cache as it is and the weights onela_paged_attention
+ *                adds up, fp32 [R][H_kv][row_pages * page].
+ *   keep         >= 1, at most dst_row_pages * page;  recent  0 .. keep.
+ *   dst_k, dst_v, dst_table
+ *                the pool copied to (pages of the same size; it may be the
+ *                same pool) and int32 [R][dst_row_pages].  The destination
+ *                pages in use must be distinct from one another and from
+ *                every source page in use.
+ *   dst_lengths  int32 [R], written: n.
+ *   dst_mass     fp32 [R][H_kv][dst_row_pages * page], its first n entries written.
+ *   kept         int32 [R][H_kv][keep] or NULL: the kept positions in order, -1
+ *                after the n-th.
+ * Sources are left as they are: the caller frees their pages.
+ *   scratch      at least onela_cache_evict_scratch_bytes(cfg) bytes.
+ * Errors: ONELA_ERR_ARG, ONELA_ERR_SCRATCH, ONELA_ERR_CUDA. */
+typedef struct {
+  int32_t R, H_kv, d;
+  int32_t dtype;
+  int32_t page, pages, row_pages;
+  int32_t dst_pages, dst_row_pages;
+  int32_t keep, recent;
+  int32_t device;
+} onela_cache_evict_config;
+ONELA_API size_t onela_cache_evict_scratch_bytes(const onela_cache_evict_config *cfg);
+ONELA_API int onela_cache_evict(const onela_cache_evict_config *cfg, const void *k_pool, const void *v_pool,
+                                const int32_t *table, const int32_t *lengths, const float *mass, void *dst_k,
+                                void *dst_v, const int32_t *dst_table, int32_t *dst_lengths, float *dst_mass,
+                                int32_t *kept, void *scratch, size_t scratch_bytes, int32_t *status,
+                                onela_stream stream);
+
+/* The norms around a block, fused with its gate and residual scale.  For each
+ * of N rows of D channels, y being the block's output:
+ *     u  = y * rsqrt(mean_group(y^2) + eps) * w_post    (with w_post)
+ *     u  = u * act(gate)                                (with gate)
+ *     x' = x + alpha * scale * u                        (x, scale: if given)
+ *     n' = x' * rsqrt(mean(x'^2) + eps) * w_pre         (with w_pre)
+ * group = D is the norm after a block; group = d_v is the per-head norm of a
+ * GDN layer's o, which onela_decode_step writes in fp32.  y NULL leaves only
+ * the norm before a block: x' = x (no gate, w_post or scale then).  All of it
+ * is computed in fp32 and rounded once per output: n' is the norm of the
+ * unrounded x'.
+ *   N             >= 0 (0: nothing to do);  D  1 .. 32768;  group divides D.
+ *   y_dtype       of y;  dtype  of gate, x, x_out and n_out.
+ *   act           ONELA_ACT_*, of the gate.
+ *   y_stride, gate_stride, x_stride   elements between rows (>= D).
+ *   w_post        fp32 [group], the same for every group;  scale, w_pre  fp32 [D].
+ *   x_out, n_out  [N][D] dense; x_out may be NULL if n_out is wanted alone,
+ *                 and may equal x when x is dense.  n_out goes with w_pre.
+ * Errors: ONELA_ERR_ARG, ONELA_ERR_CUDA. */
+enum { ONELA_ACT_NONE = 0, ONELA_ACT_SIGMOID = 1, ONELA_ACT_SILU = 2 };
+typedef struct {
+  int64_t N;
+  int64_t y_stride, gate_stride, x_stride;
+  int32_t D, group;
+  int32_t y_dtype, dtype;
+  int32_t act;
+  int32_t device;
+  float alpha, eps;
+} onela_block_norm_config;
+ONELA_API int onela_block_norm(const onela_block_norm_config *cfg, const void *y, const void *gate, const void *x,
+                               const float *w_post, const float *scale, const float *w_pre, void *x_out,
+                               void *n_out, onela_stream stream);
 
 /* Static description of a return code (never NULL). */
 ONELA_API const char *onela_error_string(int code);

@@ -196,7 +196,8 @@ const char *onela_error_string(int code) {
     case ONELA_ERR_PARENT: return "parent index outside [0, W_prev) seen on the device";
     case ONELA_ERR_CUDA: return "CUDA call failed";
     case ONELA_ERR_UNSUPPORTED: return "kernel does not support this shape";
-    case ONELA_ERR_SCRATCH: return "decode does not fit in the 32 MiB array of onela_decode_step_noalloc";
+    case ONELA_ERR_SCRATCH: 
+      return "decode does not fit in the 32 MiB array of onela_decode_step_noalloc, or the caller's scratch is too small";
     case ONELA_ERR_TIMEOUT: return "a bounded wait inside a kernel ran out; the outputs since the last check are void";
     default: return "unknown error";
   }
