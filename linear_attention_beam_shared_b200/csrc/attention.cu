@@ -23,25 +23,12 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float
 __device__ __forceinline__ void store_f(float *p, float x) { *p = x; }
 __device__ __forceinline__ void store_f(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
-}
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-// exp2(a - b) for a maximum b that may be -inf (nothing seen yet): 0 then.
-__device__ __forceinline__ float exp2_sub(float a, float b) { return b == -CUDART_INF_F ? 0.f : exp2f(a - b); }
-
 constexpr int kThreads = 128;
 constexpr int kRows = 8;   // query rows per CTA
 constexpr int kToks = 32;  // tokens per step
 
-// The general kernel: any d, fp32 or bf16.  A CTA takes one piece of a prompt,
-// one key-value head and 8 query rows; per step of 32 tokens K and V rows go
+// The general kernel: any d, fp32 or bf16.  A CTA takes one part of the
+// prompts, one key-value head and 8 query rows; per step of 32 tokens K and V rows go
 // through shared memory as fp32, each warp forms two rows' scores (lane =
 // token), and each thread keeps one or two columns of the 8 outputs.
 template <typename T, bool kVec>
@@ -56,20 +43,16 @@ __global__ void __launch_bounds__(kThreads) attn_simt(AttnParams p) {
   float *qs = smem, *ks = qs + kRows * dp, *vs = ks + kToks * dk;
 
   const int rt = blockIdx.x % p.row_tiles, uh = blockIdx.x / p.row_tiles;
-  const int h = uh % p.Hkv, u = uh / p.Hkv;
+  const int h = uh % p.Hkv;
   ptx::pdl_launch_dependents();
-  int r, lo, hi;
-  if (p.direct) {  // one piece per request, an empty one included: its rows are written here
-    r = u;
-    lo = 0;
-    hi = prompt_len(p, r);
-  } else if (!plan_unit<kThreads>(p, plan, u, r, lo, hi)) {
-    return;
-  }
-  if (h == 0 && rt == 0 && lo == 0 && tid == 0 && p.lengths[r] != prompt_len(p, r)) set_status(p.status, kStatusLength);
-
+  PlanWalk walk;
+  walk.begin<kThreads>(p, plan, uh / p.Hkv);
   const T *q = static_cast<const T *>(p.q), *k = static_cast<const T *>(p.k), *v = static_cast<const T *>(p.v);
   const int m0 = rt * kRows;
+  while (walk.next(p)) {
+  const int r = walk.r, lo = walk.lo, hi = walk.hi;
+  __syncthreads();  // the previous piece's shared memory is read
+  if (p.direct && h == 0 && rt == 0 && tid == 0 && p.lengths[r] != hi) set_status(p.status, kStatusLength);
   for (int i = warp; i < kRows; i += 4) {
     const int m = m0 + i;
     const int w = m / p.G, hq = h * p.G + m % p.G;
@@ -192,13 +175,13 @@ __global__ void __launch_bounds__(kThreads) attn_simt(AttnParams p) {
       if (c1 < p.d) store_f(o + row * p.d + c1, acc1[i] * inv);
       if (tid == 0 && p.lse) p.lse[row] = corr[i] == 0.f ? -CUDART_INF_F : (ps[0][i] + log2f(corr[i])) * kLn2;
     }
-    return;
+    continue;
   }
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const int m = m0 + i;
     if (m >= p.M) continue;
-    float *po = p.part_o + part_row(p, u, h, m) * p.d;
+    float *po = p.part_o + part_row(p, walk.slot, h, m) * p.d;
     if (c0 < p.d) po[c0] = acc0[i];
     if (c1 < p.d) po[c1] = acc1[i];
   }
@@ -206,92 +189,203 @@ __global__ void __launch_bounds__(kThreads) attn_simt(AttnParams p) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int m = m0 + 2 * warp + i;
-      if (m < p.M) p.part_ml[part_row(p, u, h, m)] = make_float2(mx[i], sum[i]);
+      if (m < p.M) p.part_ml[part_row(p, walk.slot, h, m)] = make_float2(mx[i], sum[i]);
     }
+  }
   }
 }
 
-// Joins a row's pieces and the beam's own tokens: a warp per query row, lane
-// = column of d (c = lane + 32 i).  The beams' own tokens are few (a decode
-// horizon), so their scores are formed here, one token at a time.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) attn_join(AttnParams p) {
-  __shared__ PlanSmem plan;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rows = p.W * p.Hq, groups = (rows + 3) / 4;
-  const int r = blockIdx.x / groups, row = (blockIdx.x % groups) * 4 + warp;
-  int off, pieces;
-  plan_row<kThreads>(p, plan, r, off, pieces);
-  if (row == 0 && lane == 0 && p.lengths[r] != prompt_len(p, r)) set_status(p.status, kStatusLength);
-  ptx::pdl_wait();
-  if (row >= rows) return;
-  const int w = row / p.Hq, hq = row % p.Hq, h = hq / p.G, m = w * p.G + hq % p.G;
+// N consecutive elements as floats.
+template <int N, bool kVec>
+__device__ __forceinline__ void ldn(const float *p, float (&v)[N]) {
+  if constexpr (kVec && N >= 4) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 a = *reinterpret_cast<const float4 *>(p + i);
+      v[i] = a.x;
+      v[i + 1] = a.y;
+      v[i + 2] = a.z;
+      v[i + 3] = a.w;
+    }
+  } else if constexpr (kVec && N == 2) {
+    const float2 a = *reinterpret_cast<const float2 *>(p);
+    v[0] = a.x;
+    v[1] = a.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = p[i];
+  }
+}
+template <int N, bool kVec>
+__device__ __forceinline__ void ldn(const __nv_bfloat16 *p, float (&v)[N]) {
+  static_assert(kVec && N % 2 == 0, "pairs");
+  uint32_t u[N / 2];
+  if constexpr (N == 8) *reinterpret_cast<uint4 *>(u) = *reinterpret_cast<const uint4 *>(p);
+  else if constexpr (N == 4) *reinterpret_cast<uint2 *>(u) = *reinterpret_cast<const uint2 *>(p);
+  else u[0] = *reinterpret_cast<const uint32_t *>(p);
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    v[2 * i] = __uint_as_float(u[i] << 16);
+    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
 
-  float acc[8], mx = -CUDART_INF_F, sum = 0.f;
+// A lane's columns of a row of d: with kD (64, 128 or 256) known, kD / 32
+// consecutive ones; otherwise columns lane + 32 i.
+template <int kD>
+struct Cols {
+  static constexpr int kN = kD ? kD / 32 : 8;
+  template <typename T>
+  static __device__ __forceinline__ void load(const T *row, int lane, int d, float (&v)[kN]) {
+    if constexpr (kD) {
+      ldn<kN, true>(row + lane * kN, v);
+    } else {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-  for (int c0 = 0; c0 < pieces; c0 += 32) {
-    // One piece's (maximum, sum) per lane, then the outputs weighted by them.
-    float2 ml = make_float2(-CUDART_INF_F, 0.f);
-    if (c0 + lane < pieces) ml = p.part_ml[part_row(p, off + c0 + lane, h, m)];
-    const float mnew = fmaxf(mx, warp_max(ml.x));
-    const float f = exp2_sub(mx, mnew), e = exp2_sub(ml.x, mnew);
-    sum = sum * f + warp_sum(ml.y * e);
-    mx = mnew;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] *= f;
-    const int n = min(32, pieces - c0);
-    for (int j = 0; j < n; ++j) {
-      const float ej = __shfl_sync(0xffffffffu, e, j);
-      const float *po = p.part_o + part_row(p, off + c0 + j, h, m) * p.d;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c = lane + 32 * i;
-        if (c < p.d) acc[i] += ej * po[c];
-      }
+      for (int i = 0; i < kN; ++i) v[i] = lane + 32 * i < d ? to_f(row[lane + 32 * i]) : 0.f;
     }
   }
-  if (p.bk) {
-    const T *q = static_cast<const T *>(p.q) + ((int64_t)r * p.W + w) * p.q_stride + (int64_t)hq * p.d;
-    const T *bk = static_cast<const T *>(p.bk), *bv = static_cast<const T *>(p.bv);
-    float qv[8];
+  template <typename T>
+  static __device__ __forceinline__ void store(T *row, int lane, int d, const float (&v)[kN]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) qv[i] = lane + 32 * i < p.d ? to_f(q[lane + 32 * i]) : 0.f;
+    for (int i = 0; i < kN; ++i) {
+      const int c = kD ? lane * kN + i : lane + 32 * i;
+      if (kD || c < d) store_f(row + c, v[i]);
+    }
+  }
+};
+
+// Joins a row's pieces and the beam's own tokens.  kWpr warps share a query
+// row: 1 when there are rows enough to fill the SMs, 8 when a few rows have
+// many pieces (64 rows of 18 pieces: 8 warps halve the time).  The beams' own tokens are few
+// (a decode horizon) and differ from beam to beam, so their scores are formed
+// here by the warp, four tokens at a time.
+template <typename T, int kD, int kWpr>
+__global__ void __launch_bounds__(kWpr == 1 ? 128 : kWpr * 32) attn_join(AttnParams p) {
+  constexpr int kBlock = kWpr == 1 ? 128 : kWpr * 32, kRowsPer = kBlock / 32 / kWpr;
+  using C = Cols<kD>;
+  constexpr int N = C::kN;
+  __shared__ PlanSmem plan;
+  __shared__ float2 wml[kWpr];
+  __shared__ float wacc[kWpr == 1 ? 1 : kWpr][kWpr == 1 ? 1 : 256];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int part = kWpr == 1 ? 0 : warp;
+  const int rows = p.W * p.Hq, groups = (rows + kRowsPer - 1) / kRowsPer;
+  const int r = blockIdx.x / groups, row = (blockIdx.x % groups) * kRowsPer + (kWpr == 1 ? warp : 0);
+  int off, pieces;
+  plan_row<kBlock>(p, plan, r, off, pieces);
+  if (row == 0 && part == 0 && lane == 0 && p.lengths[r] != prompt_len(p, r)) set_status(p.status, kStatusLength);
+  const bool live = row < rows;
+  const int w = live ? row / p.Hq : 0, hq = live ? row % p.Hq : 0, h = hq / p.G, m = w * p.G + hq % p.G;
+
+  float acc[N], mx = -CUDART_INF_F, sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) acc[i] = 0.f;
+  // The beam's own tokens first: nothing of them comes from the split kernel,
+  // which may still be running.
+  if (p.bk && live) {
+    const T *bk = static_cast<const T *>(p.bk), *bv = static_cast<const T *>(p.bv);
+    float qv[N];
+    C::load(static_cast<const T *>(p.q) + ((int64_t)r * p.W + w) * p.q_stride + (int64_t)hq * p.d, lane, p.d, qv);
     const int bcap = p.brow_pages * p.bpage, given = p.blengths[(int64_t)r * p.W + w];
     const int n = given < 0 ? 0 : (given > bcap ? bcap : given);
     if (n != given && lane == 0) set_status(p.status, kStatusLength);
     const int32_t *tab = p.btable + ((int64_t)r * p.W + w) * p.brow_pages;
-    for (int t = 0; t < n; ++t) {
-      const int pg = tab[t / p.bpage];
-      if (pg < 0 || pg >= p.bpages) {
-        if (lane == 0) set_status(p.status, kStatusPage);
-        continue;
-      }
-      const int64_t at = (((int64_t)pg * p.Hkv + h) * p.bpage + t % p.bpage) * p.d;
-      float s = 0.f, vv[8];
+    for (int t0 = 4 * part; t0 < n; t0 += 4 * kWpr) {
+      float s[4], vv[4][N];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c = lane + 32 * i;
-        vv[i] = 0.f;
-        if (c < p.d) {
-          s += qv[i] * to_f(bk[at + c]);
-          vv[i] = to_f(bv[at + c]);
+      for (int j = 0; j < 4; ++j) {
+        const int t = t0 + j;
+        s[j] = -CUDART_INF_F;
+#pragma unroll
+        for (int i = 0; i < N; ++i) vv[j][i] = 0.f;
+        if (t < n) {
+          const int pg = tab[t / p.bpage];
+          if (pg >= 0 && pg < p.bpages) {
+            const int64_t at = (((int64_t)pg * p.Hkv + h) * p.bpage + t % p.bpage) * p.d;
+            float kk[N];
+            C::load(bk + at, lane, p.d, kk);
+            C::load(bv + at, lane, p.d, vv[j]);
+            s[j] = 0.f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) s[j] += qv[i] * kk[i];
+          } else if (lane == 0) {
+            set_status(p.status, kStatusPage);
+          }
         }
       }
-      s = warp_sum(s) * p.scale_log2;
-      const float mnew = fmaxf(mx, s), f = exp2_sub(mx, mnew), e = exp2_sub(s, mnew);
-      sum = sum * f + e;
-      mx = mnew;
+      float top = mx;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = acc[i] * f + e * vv[i];
+      for (int j = 0; j < 4; ++j) {
+        // A missing token's -inf stays -inf through the sum over lanes.
+        s[j] = warp_sum(s[j]) * p.scale_log2;
+        top = fmaxf(top, s[j]);
+      }
+      const float f = exp2_sub(mx, top);
+      mx = top;
+      sum *= f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[i] *= f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float e = exp2_sub(s[j], mx);
+        sum += e;
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] += e * vv[j][i];
+      }
     }
   }
+  ptx::pdl_wait();
+  if (live) {
+    for (int c0 = 0; c0 < pieces; c0 += 32 * kWpr) {
+      // One piece's (maximum, sum) per lane, then the outputs weighted by them.
+      const int mine = c0 + lane * kWpr + part;
+      float2 ml = make_float2(-CUDART_INF_F, 0.f);
+      if (mine < pieces) ml = p.part_ml[part_row(p, off + mine, h, m)];
+      const float mnew = fmaxf(mx, warp_max(ml.x));
+      const float f = exp2_sub(mx, mnew), e = exp2_sub(ml.x, mnew);
+      sum = sum * f + warp_sum(ml.y * e);
+      mx = mnew;
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[i] *= f;
+      const int n = (min(32 * kWpr, pieces - c0) - part + kWpr - 1) / kWpr;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        const float ej = __shfl_sync(0xffffffffu, e, j);
+        float x[N];
+        C::load(p.part_o + part_row(p, off + c0 + j * kWpr + part, h, m) * p.d, lane, p.d, x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] += ej * x[i];
+      }
+    }
+  }
+  if constexpr (kWpr > 1) {
+    // Warps' results through shared memory, joined by the first.
+    if (lane == 0) wml[warp] = make_float2(mx, sum);
+#pragma unroll
+    for (int i = 0; i < N; ++i) wacc[warp][lane + 32 * i] = acc[i];
+    __syncthreads();
+    if (warp != 0) return;
+    float top = -CUDART_INF_F;
+#pragma unroll
+    for (int j = 0; j < kWpr; ++j) top = fmaxf(top, wml[j].x);
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < kWpr; ++j) {
+      const float f = exp2_sub(wml[j].x, top);
+      sum += wml[j].y * f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[i] += wacc[j][lane + 32 * i] * f;
+    }
+    mx = top;
+  }
+  if (!live) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int64_t orow = ((int64_t)r * p.W + w) * p.Hq + hq;
-  T *o = static_cast<T *>(p.o) + orow * p.d;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (lane + 32 * i < p.d) store_f(o + lane + 32 * i, acc[i] * inv);
+  for (int i = 0; i < N; ++i) acc[i] *= inv;
+  C::store(static_cast<T *>(p.o) + orow * p.d, lane, p.d, acc);
   if (lane == 0) {
     const float l2 = sum == 0.f ? -CUDART_INF_F : mx + log2f(sum);
     if (p.lse) p.lse[orow] = l2 * kLn2;
@@ -314,25 +408,22 @@ __global__ void __launch_bounds__(kThreads) attn_mass(AttnParams p) {
   p.mass_out[at] = p.mass ? p.mass[at] + t : t;
 }
 
-template <typename F, typename... A>
-cudaError_t launch(F *f, unsigned grid, unsigned threads, size_t smem, bool pdl, cudaStream_t s, A... a) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, f, a...);
-}
-
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// The tensor-core kernels take bf16 with d in {64, 128, 256}; the pools' and
+// q's rows must lie on 16-byte boundaries (pointers not yet known: assumed).
+bool tc_fits(const onela_attention_config &c, const AttnParams &p) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v) | reinterpret_cast<uintptr_t>(p.q);
+  return c.dtype == ONELA_BF16 && (c.d == 64 || c.d == 128 || c.d == 256) && c.q_stride % 8 == 0 && (at & 15) == 0;
+}
+
+AttnKind choose(const onela_attention_config &c, const AttnParams &p) {
+  if (c.kernel == ONELA_KERNEL_SIMT || !tc_fits(c, p) || p.M > 16) return kAttnSimt;
+  return kAttnNarrow;
+}
+
 // Chooses the division and lays out the scratch; the bytes needed.
-size_t plan_call(const onela_attention_config &c, bool want_mass, AttnParams &p, uint8_t *scratch) {
+size_t plan_call(const onela_attention_config &c, bool want_mass, AttnParams &p, uint8_t *scratch, AttnKind &used) {
   p.R = c.R;
   p.W = c.W;
   p.Hq = c.H_q;
@@ -349,22 +440,21 @@ size_t plan_call(const onela_attention_config &c, bool want_mass, AttnParams &p,
   p.brow_pages = c.beam_row_pages;
   p.q_stride = c.q_stride;
   p.scale_log2 = c.scale * kLog2e;
-  p.rows = kRows;
-  p.row_tiles = (p.M + kRows - 1) / kRows;
-  p.tile = kToks;
-  p.min_chunk = 128;
-  // About four CTAs for every SM, fewer and longer pieces where the heads
-  // and rows alone give as many.
+  const AttnKind kind = choose(c, p);
+  p.rows = kind == kAttnNarrow ? 16 : kRows;
+  p.tile = kind == kAttnNarrow ? 64 : kToks;
+  p.row_tiles = (p.M + p.rows - 1) / p.rows;
+  // Parts per (head, row tile): the CTAs of a wave spread over them, rounded
+  // so that the last wave is full, and no more than there can be tiles.
   const long long groups = (long long)p.Hkv * p.row_tiles;
-  const long long slots = 4 * kAttnSMs;
-  long long target = (slots + groups - 1) / groups;
-  const long long most = (long long)p.R * ((p.cap + p.min_chunk - 1) / p.min_chunk);
-  if (target > most) target = most;
-  p.target = (int)target;
-  const long long by_len = most;
-  p.units = (int)(target + p.R < by_len ? target + p.R : by_len);
-  p.direct = p.cap <= p.min_chunk && c.beam_row_pages == 0 && !want_mass;
-  if (p.direct) p.units = p.R;
+  const long long slots = (kind == kAttnNarrow ? 2 : 4) * kAttnSMs;
+  const long long most = (long long)p.R * ((p.cap + p.tile - 1) / p.tile);
+  long long parts = slots / groups;
+  if (parts < 1) parts = 1;
+  if (parts > most) parts = most;
+  p.parts = (int)parts;
+  p.direct = p.cap <= 256 && c.beam_row_pages == 0 && !want_mass;
+  if (p.direct) p.parts = p.R;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     uint8_t *q = scratch + at;
@@ -372,7 +462,7 @@ size_t plan_call(const onela_attention_config &c, bool want_mass, AttnParams &p,
     return q;
   };
   if (!p.direct) {
-    const size_t rows = (size_t)p.units * p.Hkv * p.M;
+    const size_t rows = (size_t)(p.parts + p.R) * p.Hkv * p.M;
     p.part_o = reinterpret_cast<float *>(take(rows * p.d * 4));
     p.part_ml = reinterpret_cast<float2 *>(take(rows * 8));
   }
@@ -380,38 +470,78 @@ size_t plan_call(const onela_attention_config &c, bool want_mass, AttnParams &p,
     p.lse2 = reinterpret_cast<float *>(take((size_t)p.R * p.Hkv * p.M * 4));
     p.scores = reinterpret_cast<float *>(take((size_t)p.R * p.Hkv * p.M * p.cap * 4));
   }
+  used = kind;
   return at;
 }
 
 template <typename T>
-cudaError_t run(const AttnParams &p, bool vec, cudaStream_t s) {
+cudaError_t run_simt(const AttnParams &p, bool vec, cudaStream_t s) {
   const int dp = (p.d + 3) & ~3;
   const size_t smem = (size_t)(kRows * dp + kToks * (dp + 4) + kToks * dp) * 4;
   auto f = vec ? attn_simt<T, true> : attn_simt<T, false>;
-  cudaError_t e = ensure_smem_limit((const void *)f, smem);
+  const cudaError_t e = ensure_smem_limit((const void *)f, smem);
   if (e != cudaSuccess) return e;
-  e = launch(f, (unsigned)((long long)p.units * p.Hkv * p.row_tiles), kThreads, smem, false, s, p);
+  return launch_kernel(f, (unsigned)((long long)p.parts * p.Hkv * p.row_tiles), kThreads, smem, false, s, p);
+}
+
+template <typename T, int kD>
+cudaError_t run_join_d(const AttnParams &p, cudaStream_t s) {
+  const int rows = p.W * p.Hq;
+  // Eight warps a row while that is at most about one wave of warps.
+  if ((long long)p.R * rows <= 8 * kAttnSMs)
+    return launch_kernel(attn_join<T, kD, 8>, (unsigned)(p.R * rows), 256, 0, true, s, p);
+  return launch_kernel(attn_join<T, kD, 1>, (unsigned)((long long)p.R * ((rows + 3) / 4)), 128, 0, true, s, p);
+}
+
+template <typename T>
+cudaError_t run_join(const AttnParams &p, cudaStream_t s) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.bk) |
+                       reinterpret_cast<uintptr_t>(p.bv) | reinterpret_cast<uintptr_t>(p.o);
+  if ((at & 15) == 0 && p.q_stride * sizeof(T) % 16 == 0) {
+    if (p.d == 64) return run_join_d<T, 64>(p, s);
+    if (p.d == 128) return run_join_d<T, 128>(p, s);
+    if (p.d == 256) return run_join_d<T, 256>(p, s);
+  }
+  return run_join_d<T, 0>(p, s);
+}
+
+template <typename T>
+cudaError_t run(const AttnParams &p, AttnKind kind, bool vec, cudaStream_t s) {
+  cudaError_t e;
+  if (kind == kAttnNarrow) {
+    e = launch_attn_narrow(p, s);
+  } else {
+    e = run_simt<T>(p, vec, s);
+  }
   if (e != cudaSuccess || p.direct) return e;
-  e = launch(attn_join<T>, (unsigned)((long long)p.R * ((p.W * p.Hq + 3) / 4)), kThreads, 0, true, s, p);
+
+  e = run_join<T>(p, s);
   if (e != cudaSuccess || !p.mass_out) return e;
-  return launch(attn_mass, (unsigned)((long long)p.R * p.Hkv * ((p.cap + kThreads - 1) / kThreads)), kThreads, 0, true,
+  return launch_kernel(attn_mass, (unsigned)((long long)p.R * p.Hkv * ((p.cap + kThreads - 1) / kThreads)), kThreads, 0, true,
                 s, p);
 }
 
 }  // namespace
 
-bool attention_tc_supports(const onela_attention_config &, const AttnParams &) { return false; }
+bool attention_tc_supports(const onela_attention_config &c, const AttnParams &p) { return tc_fits(c, p); }
 
 size_t attention_scratch_bytes(const onela_attention_config &c, bool want_mass) {
-  AttnParams p = {};
-  return plan_call(c, want_mass, p, nullptr);
+  // The larger of the two layouts a call may use: which kernel it takes can
+  // depend on its pointers.
+  AttnParams p = {}, g = {};
+  AttnKind kind;
+  onela_attention_config general = c;
+  general.kernel = ONELA_KERNEL_SIMT;
+  const size_t a = plan_call(c, want_mass, p, nullptr, kind), b = plan_call(general, want_mass, g, nullptr, kind);
+  return a > b ? a : b;
 }
 
 cudaError_t launch_attention(const onela_attention_config &c, AttnParams &p, void *scratch, cudaStream_t s) {
-  plan_call(c, p.mass_out != nullptr, p, static_cast<uint8_t *>(scratch));
+  AttnKind kind;
+  plan_call(c, p.mass_out != nullptr, p, static_cast<uint8_t *>(scratch), kind);
   const int es = c.dtype == ONELA_BF16 ? 2 : 4;
   const bool vec = (c.d * es) % 16 == 0 && ((reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v)) & 15) == 0;
-  return c.dtype == ONELA_BF16 ? run<__nv_bfloat16>(p, vec, s) : run<float>(p, vec, s);
+  return c.dtype == ONELA_BF16 ? run<__nv_bfloat16>(p, kind, vec, s) : run<float>(p, kind, vec, s);
 }
 
 }  // namespace onela

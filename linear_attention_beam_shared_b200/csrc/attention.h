@@ -5,6 +5,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <math_constants.h>
 #include <stdint.h>
 
 namespace onela {
@@ -32,13 +33,12 @@ struct AttnParams {
   void *o;
   float *lse;
   int32_t *status;
-  // Division of the prompts (plan_* below): pieces are multiples of `tile`
-  // tokens, at least min_chunk (but for a request's last), and there are at
-  // most `units` of them.
-  int tile, min_chunk, target, units;
+  // Division of the prompts (plan_* below) into tiles of `tile` tokens, over
+  // `parts` CTAs for every (key-value head, row tile).
+  int tile, parts;
   int rows, row_tiles;  // query rows per CTA, and CTAs for the M rows
-  int direct;           // one piece per request and no beam segment: the split kernel writes o itself
-  // Scratch: per (unit, key-value head, row) the unnormalised output and
+  int direct;           // a CTA per request and no beam segment: the split kernel writes o itself
+  // Scratch: per (slot, key-value head, row) the unnormalised output and
   // (maximum, sum); lse2 [R][Hkv][M] and scores [R][Hkv][M][cap] for the mass.
   float *part_o;
   float2 *part_ml;
@@ -51,111 +51,177 @@ __device__ __forceinline__ int prompt_len(const AttnParams &p, int r) {
   return n < 0 ? 0 : (n > p.cap ? p.cap : n);
 }
 
-// The prompts are cut into pieces of about the same size whatever their
-// lengths, so that a batch of very different lengths keeps every SM busy:
-// with T tokens in all and `target` pieces wanted, a piece has about T /
-// target tokens, a request of n tokens ceil(n / that) pieces.  Every CTA
-// derives the division from the lengths itself (they live on the device and
-// the host never waits for them), which costs one pass over R integers.
+// The prompts, cut into tiles, are laid end to end: T tiles in all, and part
+// c of n takes tiles floor(c T / n) .. floor((c + 1) T / n) - 1 of them.  So
+// every CTA has the same work to within a tile, whatever the lengths of a batch; a
+// part may end inside one request and begin inside another.  What part c
+// finds for request r goes to slot c + r: walking along the tiles either c or
+// r grows by one at each border, so a slot has one writer, and a request's
+// slots are consecutive.  Every CTA derives the division from the lengths
+// itself (they live on the device and the host never waits for them), which
+// costs one pass over R integers.
 struct PlanSmem {
   long long tot[32];
-  int cnt[32];
-  int r, c, pieces, off;
+  int r;
+  long long base;
 };
 
-// Block-wide: fills sm.cnt with the warps' piece counts; returns the tokens
-// per piece, and in `before` / `mine` the pieces of the requests before this
-// thread's stretch of requests and in it.
+__device__ __forceinline__ int tiles_of(const AttnParams &p, int r) { return (prompt_len(p, r) + p.tile - 1) / p.tile; }
+
+// Block-wide: the tiles of all requests, and of those before this thread's
+// stretch of requests [r0, r1).
 template <int kThreads>
-__device__ __forceinline__ int plan_scan(const AttnParams &p, PlanSmem &sm, int &before, int &mine) {
+__device__ __forceinline__ long long plan_scan(const AttnParams &p, PlanSmem &sm, int &r0, int &r1, long long &before) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kWarps = kThreads / 32;
   const int seg = (p.R + kThreads - 1) / kThreads;
-  const int r0 = min(p.R, tid * seg), r1 = min(p.R, r0 + seg);
-  long long t = 0;
-  for (int r = r0; r < r1; ++r) t += prompt_len(p, r);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  if (lane == 0) sm.tot[warp] = t;
-  if (tid == 0) sm.r = -1;
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += sm.tot[w];
-  long long want = (total + p.target - 1) / p.target;
-  if (want < p.min_chunk) want = p.min_chunk;
-  if (want > p.cap) want = p.cap;
-  const int chunk = (int)((want + p.tile - 1) / p.tile) * p.tile;
-  int c = 0;
-  for (int r = r0; r < r1; ++r) c += (prompt_len(p, r) + chunk - 1) / chunk;
-  mine = c;
-  int incl = c;
+  r0 = min(p.R, tid * seg);
+  r1 = min(p.R, r0 + seg);
+  long long mine = 0;
+  for (int r = r0; r < r1; ++r) mine += tiles_of(p, r);
+  long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, incl, o);
+    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += x;
   }
-  if (lane == 31) sm.cnt[warp] = incl;
+  if (lane == 31) sm.tot[warp] = incl;
   __syncthreads();
-  before = incl - c;
-  for (int w = 0; w < warp; ++w) before += sm.cnt[w];
-  return chunk;
+  long long total = 0;
+  before = incl - mine;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += sm.tot[w];
+    total += sm.tot[w];
+  }
+  return total;
 }
 
-// Piece `u`: its request and token range [lo, hi); false past the last piece.
-template <int kThreads>
-__device__ __forceinline__ bool plan_unit(const AttnParams &p, PlanSmem &sm, int u, int &r, int &lo, int &hi) {
-  int before, mine;
-  const int chunk = plan_scan<kThreads>(p, sm, before, mine);
-  if (u >= before && u < before + mine) {
-    const int seg = (p.R + kThreads - 1) / kThreads;
-    int at = before, q = threadIdx.x * seg;
-    for (;; ++q) {
-      const int n = (prompt_len(p, q) + chunk - 1) / chunk;
-      if (u < at + n) {
+// Part `c`: walks its pieces.  next() gives the next request and its token
+// range [lo, hi); false at the end.  Every thread holds the same values.
+struct PlanWalk {
+  long long at, end, base;  // tiles: the next one, the part's end, the request's first
+  int r, lo, hi, slot;
+  template <int kThreads>
+  __device__ __forceinline__ void begin(const AttnParams &p, PlanSmem &sm, int c) {
+    if (p.direct) {  // part c is request c
+      r = c - 1;
+      at = 0;
+      end = 1;
+      base = 0;
+      return;
+    }
+    int r0, r1;
+    long long before;
+    const long long total = plan_scan<kThreads>(p, sm, r0, r1, before);
+    const long long n = total < p.parts ? total : p.parts;
+    if (c >= n) {
+      at = end = 0;
+      return;
+    }
+    at = c * total / n;
+    end = (c + 1) * total / n;
+    slot = c;
+    for (int q = r0; q < r1; ++q) {
+      const int t = tiles_of(p, q);
+      if (at >= before && at < before + t) {  // exactly one thread and request
         sm.r = q;
-        sm.c = u - at;
-        sm.pieces = n;
-        break;
+        sm.base = before;
       }
-      at += n;
+      before += t;
+    }
+    __syncthreads();
+    r = sm.r - 1;
+    base = sm.base;
+    slot = c + r;
+  }
+  __device__ __forceinline__ bool next(const AttnParams &p) {
+    if (at >= end) return false;
+    if (p.direct) {
+      ++r;
+      at = end;
+      lo = 0;
+      hi = prompt_len(p, r);
+      return true;
+    }
+    for (;;) {
+      ++r;
+      ++slot;
+      const int len = prompt_len(p, r), t = (len + p.tile - 1) / p.tile;
+      if (at < base + t) {
+        const long long stop = end < base + t ? end : base + t;
+        lo = (int)(at - base) * p.tile;
+        hi = min(len, (int)(stop - base) * p.tile);
+        at = stop;
+        base += t;
+        return true;
+      }
+      base += t;
     }
   }
-  __syncthreads();
-  r = sm.r;
-  if (r < 0) return false;
-  const int len = prompt_len(p, r);
-  const int per = ((len + sm.pieces - 1) / sm.pieces + p.tile - 1) / p.tile * p.tile;
-  lo = sm.c * per;
-  hi = min(len, lo + per);
-  return true;
-}
+};
 
-// Request r: its first piece and how many it has.
+// Request r: its first slot and how many it has.
 template <int kThreads>
 __device__ __forceinline__ void plan_row(const AttnParams &p, PlanSmem &sm, int r, int &off, int &pieces) {
-  int before, mine;
-  const int chunk = plan_scan<kThreads>(p, sm, before, mine);
-  const int seg = (p.R + kThreads - 1) / kThreads;
-  if (r / seg == (int)threadIdx.x) {
-    int at = before;
-    for (int q = threadIdx.x * seg; q < r; ++q) at += (prompt_len(p, q) + chunk - 1) / chunk;
-    sm.off = at;
-    sm.pieces = (prompt_len(p, r) + chunk - 1) / chunk;
+  int r0, r1;
+  long long before;
+  const long long total = plan_scan<kThreads>(p, sm, r0, r1, before);
+  if (r >= r0 && r < r1) {
+    for (int q = r0; q < r; ++q) before += tiles_of(p, q);
+    sm.base = before;
   }
   __syncthreads();
-  off = sm.off;
-  pieces = sm.pieces;
+  const long long first = sm.base, n = total < p.parts ? total : p.parts, t = tiles_of(p, r);
+  if (t == 0) {
+    off = pieces = 0;
+    return;
+  }
+  const long long c0 = ((first + 1) * n - 1) / total, c1 = ((first + t) * n - 1) / total;
+  off = (int)c0 + r;
+  pieces = (int)(c1 - c0) + 1;
 }
 
-// Partial results of row m of (unit, head).
-__device__ __forceinline__ int64_t part_row(const AttnParams &p, int unit, int h, int m) {
-  return ((int64_t)unit * p.Hkv + h) * p.M + m;
+// Partial results of row m of (slot, head).
+__device__ __forceinline__ int64_t part_row(const AttnParams &p, int slot, int h, int m) {
+  return ((int64_t)slot * p.Hkv + h) * p.M + m;
 }
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+// exp2(a - b) for a maximum b that may be -inf (nothing seen yet): 0 then.
+__device__ __forceinline__ float exp2_sub(float a, float b) { return b == -CUDART_INF_F ? 0.f : exp2f(a - b); }
 
 constexpr int32_t kStatusPage = 1, kStatusLength = 2;  // ONELA_STATUS_*
 __device__ __forceinline__ void set_status(int32_t *status, int32_t bit) {
   if (status) atomicOr(status, bit);
+}
+
+// Kernels of a call, chosen on the host.
+enum AttnKind { kAttnSimt = 0, kAttnNarrow = 1 };
+cudaError_t launch_attn_narrow(const AttnParams &p, cudaStream_t s);  // attention_narrow.cu
+
+template <typename... P, typename... A>
+cudaError_t launch_kernel(void (*f)(P...), unsigned grid, unsigned threads, size_t smem, bool pdl, cudaStream_t s, A... a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, f, a...);
 }
 
 }  // namespace onela
