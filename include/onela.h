@@ -477,8 +477,10 @@ enum {
   ONELA_STATUS_PAGE = 1,   /* a page number outside [0, pages) was met: the
                               token was left out (attention), not written
                               (write, evict) or copied as zeros (evict)      */
-  ONELA_STATUS_LENGTH = 2  /* a length, start or count outside what its row
+  ONELA_STATUS_LENGTH = 2, /* a length, start or count outside what its row
                               can hold was clamped, or a write fell past it */
+  ONELA_STATUS_TIMEOUT = 4 /* a bounded wait inside a kernel ran out: the
+                              outputs are void (NaN where rows are concerned) */
 };
 
 /* Attention of new tokens over the cache.  Request r has W beams (W = 1: an

@@ -27,8 +27,8 @@ from ._lib import (  # noqa: F401
     onela_status, onela_status_code, onela_steps_done,
 )
 from ._layers import (  # noqa: F401
-    ONELA_ACT_NONE, ONELA_ACT_SIGMOID, ONELA_ACT_SILU, ONELA_STATUS_LENGTH, ONELA_STATUS_PAGE, onela_block_norm,
-    onela_cache_evict, onela_cache_write, onela_paged_attention, onela_paged_attention_scratch_bytes,
+    ONELA_ACT_NONE, ONELA_ACT_SIGMOID, ONELA_ACT_SILU, ONELA_STATUS_LENGTH, ONELA_STATUS_PAGE, ONELA_STATUS_TIMEOUT,
+    onela_block_norm, onela_cache_evict, onela_cache_write, onela_paged_attention, onela_paged_attention_scratch_bytes,
 )
 
 LIB_PATH = _lib.LIB_PATH

@@ -20,7 +20,7 @@ import torch
 
 from ._lib import ONELA_KERNEL_AUTO, _check, lib
 
-ONELA_STATUS_PAGE, ONELA_STATUS_LENGTH = 1, 2
+ONELA_STATUS_PAGE, ONELA_STATUS_LENGTH, ONELA_STATUS_TIMEOUT = 1, 2, 4
 ONELA_ACT_NONE, ONELA_ACT_SIGMOID, ONELA_ACT_SILU = 0, 1, 2
 
 _i32, _i64, _f32, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p

@@ -9,7 +9,7 @@
 // it is held in fp32.
 #include "attention.h"
 
-#include <math_constants.h>
+#include <algorithm>
 
 #include "../../include/onela.h"
 #include "internal.h"
@@ -273,6 +273,8 @@ __global__ void __launch_bounds__(kWpr == 1 ? 128 : kWpr * 32) attn_join(AttnPar
   const int r = blockIdx.x / groups, row = (blockIdx.x % groups) * kRowsPer + (kWpr == 1 ? warp : 0);
   int off, pieces;
   plan_row<kBlock>(p, plan, r, off, pieces);
+  off *= p.per_slot;
+  pieces *= p.per_slot;
   if (row == 0 && part == 0 && lane == 0 && p.lengths[r] != prompt_len(p, r)) set_status(p.status, kStatusLength);
   const bool live = row < rows;
   const int w = live ? row / p.Hq : 0, hq = live ? row % p.Hq : 0, h = hq / p.G, m = w * p.G + hq % p.G;
@@ -417,9 +419,10 @@ bool tc_fits(const onela_attention_config &c, const AttnParams &p) {
   return c.dtype == ONELA_BF16 && (c.d == 64 || c.d == 128 || c.d == 256) && c.q_stride % 8 == 0 && (at & 15) == 0;
 }
 
-AttnKind choose(const onela_attention_config &c, const AttnParams &p) {
-  if (c.kernel == ONELA_KERNEL_SIMT || !tc_fits(c, p) || p.M > 16) return kAttnSimt;
-  return kAttnNarrow;
+AttnKind choose(const onela_attention_config &c, const AttnParams &p, bool want_mass) {
+  if (c.kernel == ONELA_KERNEL_SIMT || !tc_fits(c, p)) return kAttnSimt;
+  if (p.M <= 16) return kAttnNarrow;
+  return want_mass ? kAttnSimt : kAttnWide;
 }
 
 // Chooses the division and lays out the scratch; the bytes needed.
@@ -440,20 +443,38 @@ size_t plan_call(const onela_attention_config &c, bool want_mass, AttnParams &p,
   p.brow_pages = c.beam_row_pages;
   p.q_stride = c.q_stride;
   p.scale_log2 = c.scale * kLog2e;
-  const AttnKind kind = choose(c, p);
-  p.rows = kind == kAttnNarrow ? 16 : kRows;
-  p.tile = kind == kAttnNarrow ? 64 : kToks;
+  const AttnKind kind = choose(c, p, want_mass);
+  int ctas = 4 * kAttnSMs;  // that run at once
+  p.rows = kRows;
+  p.tile = kToks;
+  p.per_slot = 1;
+  if (kind == kAttnNarrow) {
+    p.rows = 16;
+    p.tile = 64;
+    ctas = 2 * kAttnSMs;
+  } else if (kind == kAttnWide) {
+    p.rows = c.d < 256 && p.M > 128 ? 256 : 128;
+    p.tile = c.d == 256 ? 64 : 128;
+    p.per_slot = c.d < 256 && p.M <= 128 ? 2 : 1;
+    ctas = kAttnSMs;
+  }
   p.row_tiles = (p.M + p.rows - 1) / p.rows;
-  // Parts per (head, row tile): the CTAs of a wave spread over them, rounded
-  // so that the last wave is full, and no more than there can be tiles.
+  // Parts per (head, row tile).  n parts take ceil(groups n / ctas) waves of
+  // T / n tiles and, for each, about as long as 4 tiles to start and finish;
+  // T is at most `most`.  The cheapest n, up to 8 waves.
   const long long groups = (long long)p.Hkv * p.row_tiles;
-  const long long slots = (kind == kAttnNarrow ? 2 : 4) * kAttnSMs;
   const long long most = (long long)p.R * ((p.cap + p.tile - 1) / p.tile);
-  long long parts = slots / groups;
-  if (parts < 1) parts = 1;
-  if (parts > most) parts = most;
-  p.parts = (int)parts;
-  p.direct = p.cap <= 256 && c.beam_row_pages == 0 && !want_mass;
+  const long long limit = std::min(most, std::max(1LL, 8LL * ctas / groups));
+  double best = 0;
+  p.parts = 1;
+  for (long long n = 1; n <= limit; ++n) {
+    const double cost = (double)((groups * n + ctas - 1) / ctas) * ((double)most / n + 4.0);
+    if (n == 1 || cost < best) {
+      best = cost;
+      p.parts = (int)n;
+    }
+  }
+  p.direct = kind != kAttnWide && p.cap <= 256 && c.beam_row_pages == 0 && !want_mass;
   if (p.direct) p.parts = p.R;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -462,7 +483,7 @@ size_t plan_call(const onela_attention_config &c, bool want_mass, AttnParams &p,
     return q;
   };
   if (!p.direct) {
-    const size_t rows = (size_t)(p.parts + p.R) * p.Hkv * p.M;
+    const size_t rows = (size_t)(p.parts + p.R) * p.per_slot * p.Hkv * p.M;
     p.part_o = reinterpret_cast<float *>(take(rows * p.d * 4));
     p.part_ml = reinterpret_cast<float2 *>(take(rows * 8));
   }
@@ -510,6 +531,8 @@ cudaError_t run(const AttnParams &p, AttnKind kind, bool vec, cudaStream_t s) {
   cudaError_t e;
   if (kind == kAttnNarrow) {
     e = launch_attn_narrow(p, s);
+  } else if (kind == kAttnWide) {
+    e = launch_attn_wide(p, s);
   } else {
     e = run_simt<T>(p, vec, s);
   }

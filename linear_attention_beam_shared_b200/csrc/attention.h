@@ -37,6 +37,7 @@ struct AttnParams {
   // `parts` CTAs for every (key-value head, row tile).
   int tile, parts;
   int rows, row_tiles;  // query rows per CTA, and CTAs for the M rows
+  int per_slot;         // results per slot (two where two warp groups share the rows)
   int direct;           // a CTA per request and no beam segment: the split kernel writes o itself
   // Scratch: per (slot, key-value head, row) the unnormalised output and
   // (maximum, sum); lse2 [R][Hkv][M] and scores [R][Hkv][M][cap] for the mass.
@@ -206,8 +207,9 @@ __device__ __forceinline__ void set_status(int32_t *status, int32_t bit) {
 }
 
 // Kernels of a call, chosen on the host.
-enum AttnKind { kAttnSimt = 0, kAttnNarrow = 1 };
+enum AttnKind { kAttnSimt = 0, kAttnNarrow = 1, kAttnWide = 2 };
 cudaError_t launch_attn_narrow(const AttnParams &p, cudaStream_t s);  // attention_narrow.cu
+cudaError_t launch_attn_wide(const AttnParams &p, cudaStream_t s);    // attention_wide.cu
 
 template <typename... P, typename... A>
 cudaError_t launch_kernel(void (*f)(P...), unsigned grid, unsigned threads, size_t smem, bool pdl, cudaStream_t s, A... a) {
