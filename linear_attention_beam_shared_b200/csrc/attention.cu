@@ -454,7 +454,7 @@ size_t plan_call(const onela_attention_config &c, bool want_mass, AttnParams &p,
     ctas = 2 * kAttnSMs;
   } else if (kind == kAttnWide) {
     p.rows = c.d < 256 && p.M > 128 ? 256 : 128;
-    p.tile = c.d == 256 ? 64 : 128;
+    p.tile = 64;
     p.per_slot = c.d < 256 && p.M <= 128 ? 2 : 1;
     ctas = kAttnSMs;
   }

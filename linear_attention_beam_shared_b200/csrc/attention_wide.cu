@@ -3,19 +3,23 @@
 // 4 grouped heads) read the same K and V.  bf16, d in {64, 128, 256}.
 //
 // At 128 rows per tile a K and V row is used 128 times for every read, so the
-// matrix products (4 d operations per row and token) and the exponentials (one per
-// row and token, 16 a clock on an SM) bound it: at d = 128 both take about 512
-// clocks for 128 rows x 64 tokens.  Both products run on tcgen05: S = Q K^T
-// with both operands in shared memory, O += P V with P in tensor memory, where the
-// softmax warps write it over the scores they read, and V as it lies in the
-// cache (token rows, an MN-major B operand).  O stays in tensor memory.
+// matrix products (4 d operations per row and token) and the exponentials
+// (one per row and token, 16 a clock on an SM) bound it: at d = 128 both take
+// about 512 clocks for 128 rows x 64 tokens.  Both products run on tcgen05: S
+// = Q K^T with both operands in shared memory, O += P V with P in tensor
+// memory, where the softmax warps write it over the scores they read, and V
+// as it lies in the cache (token rows, an MN-major B operand).  O stays in
+// tensor memory.
 //
-// Two groups of four softmax warps (thread = row) work on two score buffers, so that one group's exponentials
-// overlap the other's products.  The groups take the two
-// halves of 256 rows (kSub = 2, K and V read once for both) or, with at most
-// 128 rows, every other token tile of the same rows (kSub = 1), each with its own O
-// and its own result slot.  At d = 256 O fills half of the tensor memory,
-// so one group works through both score buffers.
+// Two groups of four softmax warps (thread = row) each own an O and two score
+// buffers of 64 tokens: while a group takes the exponentials of one buffer, the
+// tensor cores fill its other one and work for the other group.  (With one
+// buffer of 128 tokens a group, each group's products waited for its
+// exponentials and these for its products: 2.3 times slower.)  The groups take
+// the two halves of 256 rows (kSub = 2, K and V read once for both) or, with at
+// most 128 rows, every other token tile of the same rows (kSub = 1), each with
+// its own result slot.  At d = 256 O fills half of the tensor memory, so there
+// is one group.
 //
 // The running maximum that weights are taken against moves only when a row's
 // maximum grew by more than 2^8 (scores in log2 units): weights then stay
@@ -23,15 +27,19 @@
 // P is rounded to bf16 (2^-8 relative per weight at most, of the size of the
 // rounding of o itself); its sum is that of the unrounded weights, in fp32.
 //
-// Four warps gather the K and V rows with 16-byte asynchronous copies through
-// the page table into a ring of two K and two V tiles, zeros for tokens
-// that are not there; one thread issues the products.  Every wait is bounded:
-// one that runs out sets ONELA_STATUS_TIMEOUT and the results become NaN.
+// Four warps bring in the K and V rows, a quarter of a tile each, through the
+// page table into rings of K and V tiles: by TMA boxes of 16 or 8 tokens
+// where all of a warp's tokens are there and pages are multiples of 8 tokens,
+// otherwise by 16-byte asynchronous copies, zeros for tokens that are not
+// there.  (Those alone held the SM to 18 bytes a clock.)  One thread issues
+// the products.  Every wait is bounded: one that runs out sets
+// ONELA_STATUS_TIMEOUT and the results become NaN.
 #include "attention.h"
 
 #include "../../include/onela.h"
 #include "internal.h"
 #include "sm100_ptx.h"
+#include "tc_common.h"
 
 namespace onela {
 namespace {
@@ -40,28 +48,35 @@ constexpr uint64_t kWaitNs = 2000000000ull;  // bound of every wait
 constexpr float kSlack = 8.f;                // growth of the maximum, in log2, before O is rescaled
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 256;  // scores behind the outputs in tensor memory
+constexpr int TT = 64;           // tokens per tile
 
 template <int D, int kSub>
 struct Cfg {
-  static constexpr int TT = D == 256 ? 64 : 128;      // tokens per tile
-  static constexpr int kGroups = D == 256 ? 1 : 2;    // softmax groups
-  static constexpr int kSoft = kGroups * 128;
+  static constexpr int G = D == 256 ? 1 : 2;  // softmax groups
+  static constexpr int kSoft = G * 128;
   static constexpr int kThreads = kSoft + 128 + 32;
-  static constexpr int kQ = 128 * D * 2;              // bytes of 128 Q rows
-  static constexpr int kTile = TT * D * 2;            // bytes of a K or V tile
-  static constexpr int oK = kSub * kQ, oV = oK + 2 * kTile, oEnd = oV + 2 * kTile;
+  static constexpr int kStages = D == 256 ? 2 : 4;
+  static constexpr int kQ = 128 * D * 2;    // bytes of 128 Q rows
+  static constexpr int kTile = TT * D * 2;  // bytes of a K or V tile
+  static constexpr int oK = kSub * kQ, oV = oK + kStages * kTile, oEnd = oV + kStages * kTile;
   // Above half of an SM's shared memory, so that one CTA has the SM (and its
   // tensor memory) for itself.
   static constexpr int kSmem = oEnd + 1024 < 120 * 1024 ? 120 * 1024 : oEnd + 1024;
 };
 
 struct Shared {
-  uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
-  uint64_t s[2], p[2], pv[2];
+  uint64_t kfull[4], kempty[4], vfull[4], vempty[4];
+  uint64_t s[4], p[4], pv[4];  // by group and score buffer
   uint64_t q, done;
   uint32_t tmem;
-  uint32_t mask[4][4];  // by K tile (ring of 4): the tokens that are there
+  uint32_t mask[8][4];  // by tile (ring of 8) and load warp: the 16 tokens that are there
   PlanSmem plan;
+};
+
+// K and V pools as {64 elements, 1, tokens of a page, (page, head)}.
+struct Maps {
+  CUtensorMap k, v;
+  int box;  // tokens per box: 16, 8, or 0 (pages not a multiple of 8: no boxes)
 };
 
 template <int N>
@@ -72,6 +87,12 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+// 2^x for x <= kSlack; results below 2^-126 become 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 // Wait unless a wait of this thread has run out before.
 __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, bool &dead) {
@@ -84,21 +105,22 @@ __device__ __forceinline__ void wait_warp(uint64_t *bar, uint32_t parity, bool &
 }
 
 template <int D, int kSub>
-__global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(AttnParams p) {
+__global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __grid_constant__ AttnParams p,
+                                                                       const __grid_constant__ Maps maps) {
   using C = Cfg<D, kSub>;
-  constexpr int TT = C::TT, G = C::kGroups;
+  constexpr int G = C::G, NS = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Shared sh;
   uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t base = ptx::smem_u32(smem);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int rt = blockIdx.x % p.row_tiles, ch = blockIdx.x / p.row_tiles;
   const int h = ch % p.Hkv, part = ch / p.Hkv;
   const int m0 = rt * (128 * kSub);
 
   constexpr int kMmaWarp = C::kSoft / 32 + 4;
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       ptx::mbar_init(&sh.kfull[i], 4);
       ptx::mbar_init(&sh.vfull[i], 4);
       ptx::mbar_init(&sh.kempty[i], 1);
@@ -121,31 +143,36 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(AttnParam
   __syncthreads();
   ptx::tc_fence_after();
   walk.begin<C::kThreads>(p, sh.plan, part);
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
   bool dead = false;
 
   if (warp < C::kSoft / 32) {
     // ------------------------------------------------------------- softmax
     const int grp = warp >> 2, row = (warp & 3) * 32 + lane;  // thread = query row
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const int m = m0 + (kSub == 2 ? grp * 128 : 0) + row;
-    uint32_t ns[2] = {0, 0};  // jobs done on each score buffer
-    uint32_t tile0 = 0;       // K tiles of earlier pieces (the mask ring runs on)
+    const int m1 = m0 + (kSub == 2 ? grp * 128 : 0), m = m1 + row;
+    const uint32_t o_t = tmem + lanes + (G == 2 ? grp * 128 : 0);
+    uint32_t c = 0;      // jobs of this group so far: buffer c & 1, use c >> 1 of it
+    uint32_t tile0 = 0;  // tiles of earlier pieces (the mask ring runs on)
     while (walk.next(p)) {
       const int r = walk.r;
-      const int nt = (walk.hi - walk.lo + TT - 1) / TT, nj = nt * kSub;
+      const int nt = (walk.hi - walk.lo + TT - 1) / TT;
       // Every product of the last piece is done (each group waited for its
       // own): Q may be replaced.
       ptx::bar_sync(1, C::kSoft);
       if (kSub == 2 || grp == 0) {
+        // A warp brings its 32 rows, 32 16-byte chunks at a time.
         uint8_t *qd = smem + (kSub == 2 ? grp * C::kQ : 0);
-        const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q);
-        if (m < p.M) src += ((int64_t)r * p.W + m / p.G) * p.q_stride + (int64_t)(h * p.G + m % p.G) * D;
+        constexpr int kPer = D / 8;
 #pragma unroll 8
-        for (int c = 0; c < D / 8; ++c) {
+        for (int e = 0; e < kPer; ++e) {
+          const int at = e * 32 + lane, rw = (warp & 3) * 32 + at / kPer, cc = at % kPer, mm = m1 + rw;
           uint4 x = make_uint4(0, 0, 0, 0);
-          if (m < p.M) x = __ldg(reinterpret_cast<const uint4 *>(src) + c);
-          *reinterpret_cast<uint4 *>(qd + (c >> 3) * 16384 + ptx::swz128(row, c & 7)) = x;
+          if (mm < p.M)
+            x = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) +
+                                                      ((int64_t)r * p.W + mm / p.G) * p.q_stride +
+                                                      (int64_t)(h * p.G + mm % p.G) * D) + cc);
+          *reinterpret_cast<uint4 *>(qd + (cc >> 3) * 16384 + ptx::swz128(rw, cc & 7)) = x;
         }
       }
       ptx::fence_proxy_async();
@@ -153,54 +180,44 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(AttnParam
 
       float mref = -CUDART_INF_F, sum = 0.f;
       bool any = false;  // this group has a product in O
-      const uint32_t o_t = tmem + lanes + (G == 2 ? grp * 128 : 0);
-      for (int j = G == 2 ? grp : 0; j < nj; j += G) {
-        const int b = j & 1, tile = kSub == 2 ? j >> 1 : j;
+      constexpr int kStep = kSub == 1 ? G : 1;
+      for (int t = kSub == 1 ? grp : 0; t < nt; t += kStep, ++c) {
+        const int b = grp * 2 + (c & 1);
         const uint32_t s_t = tmem + lanes + kSCol + b * TT;
-        wait_warp(&sh.s[b], ns[b] & 1, dead);
-        ++ns[b];
+        wait_warp(&sh.s[b], (c >> 1) & 1, dead);
         ptx::tc_fence_after();
-        uint32_t msk[TT / 32];
-        bool full = true;
+        float x[2][32];
+        ptx::tmem_ld32(s_t, x[0]);
+        ptx::tmem_ld32(s_t + 32, x[1]);
+        const uint32_t *mk = sh.mask[(tile0 + t) & 7];
+        const uint32_t msk[2] = {mk[0] | (mk[1] << 16), mk[2] | (mk[3] << 16)};
+        ptx::tmem_ld_wait();
+        if ((msk[0] & msk[1]) != 0xffffffffu) {
 #pragma unroll
-        for (int e = 0; e < TT / 32; ++e) {
-          msk[e] = TT == 128 ? sh.mask[(tile0 + tile) & 3][e]
-                             : sh.mask[(tile0 + tile) & 3][2 * e] | (sh.mask[(tile0 + tile) & 3][2 * e + 1] << 16);
-          full = full && msk[e] == 0xffffffffu;
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[e][i] = (msk[e] >> i) & 1 ? x[e][i] : -CUDART_INF_F;
         }
-        // Pass 1: the row's maximum over the tile.
-        float top = -CUDART_INF_F;
+        float t4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-        for (int e = 0; e < TT / 32; ++e) {
-          float x[32];
-          ptx::tmem_ld32(s_t + e * 32, x);
-          ptx::tmem_ld_wait();
-          if (full) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) top = fmaxf(top, x[i]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) top = fmaxf(top, (msk[e] >> i) & 1 ? x[i] : -CUDART_INF_F);
-          }
-        }
-        top *= p.scale_log2;
+        for (int i = 0; i < 64; ++i) t4[i & 3] = fmaxf(t4[i & 3], x[i >> 5][i & 31]);
+        const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * p.scale_log2;
         // Move the reference when the maximum outgrew it (or on the first tile).
         const bool grow = top > mref + kSlack || (mref == -CUDART_INF_F && top > mref);
         if (__any_sync(0xffffffffu, grow)) {
           const float f = grow ? exp2_sub(mref, top) : 1.f;
           if (any) {
-            // The last product into O must be done: at d = 256 it is that of
-            // the other score buffer; otherwise the scores' own order says so.
-            if (G == 1) wait_warp(&sh.pv[b ^ 1], (ns[b ^ 1] - 1) & 1, dead);
+            // The group's last product into O must be done.
+            wait_warp(&sh.pv[b ^ 1], ((c - 1) >> 1) & 1, dead);
             ptx::tc_fence_after();
 #pragma unroll 1
             for (int e = 0; e < D / 16; ++e) {
-              float x[16];
+              float z[16];
               uint32_t y[16];
-              ptx::tmem_ld16(o_t + e * 16, x);
+              ptx::tmem_ld16(o_t + e * 16, z);
               ptx::tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(x[i] * f);
+              for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(z[i] * f);
               ptx::tmem_st<16>(o_t + e * 16, y);
             }
           }
@@ -210,118 +227,139 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(AttnParam
           }
         }
         any = true;
-        // Pass 2: the weights, over the scores' own columns.
+        // The weights, over the scores' own columns.
         const float off = mref == -CUDART_INF_F ? 0.f : mref;
-        float part_sum[4] = {0.f, 0.f, 0.f, 0.f};
+        float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int e = 0; e < TT / 32; ++e) {
-          float x[32];
-          uint32_t y[16];
-          ptx::tmem_ld32(s_t + e * 32, x);
-          ptx::tmem_ld_wait();
-          if (full) {
+        for (int e = 0; e < 4; ++e) {
+          uint32_t y[8];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = exp2f(fmaf(x[i], p.scale_log2, -off));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = (msk[e] >> i) & 1 ? exp2f(fmaf(x[i], p.scale_log2, -off)) : 0.f;
+          for (int i = 0; i < 8; ++i) {
+            const float a = ex2(fmaf(x[e >> 1][(e & 1) * 16 + 2 * i], p.scale_log2, -off));
+            const float bb = ex2(fmaf(x[e >> 1][(e & 1) * 16 + 2 * i + 1], p.scale_log2, -off));
+            s4[i & 3] += a + bb;
+            y[i] = pack(a, bb);
           }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            part_sum[i & 3] += x[2 * i] + x[2 * i + 1];
-            y[i] = pack(x[2 * i], x[2 * i + 1]);
-          }
-          ptx::tmem_st<16>(s_t + e * 16, y);
+          ptx::tmem_st<8>(s_t + e * 8, y);
         }
-        sum += (part_sum[0] + part_sum[1]) + (part_sum[2] + part_sum[3]);
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         ptx::mbar_arrive(&sh.p[b]);
+        sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
       }
       tile0 += nt;
       // The outputs, unnormalised, and (maximum, sum) to the piece's slot.
       const int slot = G == 2 && kSub == 1 ? 2 * walk.slot + grp : walk.slot;
       const int64_t pr = part_row(p, slot, h, m);
       if (any) {
-        const int bl = G == 2 ? grp : (nj - 1) & 1;  // score buffer of the group's last job
-        wait_warp(&sh.pv[bl], (ns[bl] - 1) & 1, dead);
+        wait_warp(&sh.pv[grp * 2 + ((c - 1) & 1)], ((c - 1) >> 1) & 1, dead);
         ptx::tc_fence_after();
+      }
 #pragma unroll 1
-        for (int e = 0; e < D / 32; ++e) {
-          float x[32];
-          ptx::tmem_ld32(o_t + e * 32, x);
+      for (int e = 0; e < D / 32; ++e) {
+        float z[32];
+        if (any) {
+          ptx::tmem_ld32(o_t + e * 32, z);
           ptx::tmem_ld_wait();
-          if (m < p.M) {
-            float4 *out = reinterpret_cast<float4 *>(p.part_o + pr * D + e * 32);
+        }
+        if (m < p.M) {
+          float *out = p.part_o + pr * D + e * 32;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) out[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+          for (int i = 0; i < 32; i += 8) {
+            float y[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) y[q] = any ? z[i + q] : 0.f;
+            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + i), "f"(y[0]), "f"(y[1]),
+                         "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7])
+                         : "memory");
           }
         }
-        ptx::tc_fence_before();
-      } else if (m < p.M) {
-        float4 *out = reinterpret_cast<float4 *>(p.part_o + pr * D);
-        for (int i = 0; i < D / 4; ++i) out[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       }
+      if (any) ptx::tc_fence_before();
       if (m < p.M) p.part_ml[pr] = dead ? make_float2(0.f, CUDART_NAN_F) : make_float2(mref, sum);
     }
   } else if (warp < kMmaWarp) {
     // -------------------------------------------------------------- loads
     const int lw = warp - C::kSoft / 32;
-    constexpr int kTokW = TT / 4;                // tokens of a tile this warp copies
-    constexpr int kPer = D * 2 / 16;             // 16-byte chunks of a row
+    constexpr int kTokW = TT / 4;     // tokens of a tile this warp brings
+    constexpr int kPer = D * 2 / 16;  // 16-byte chunks of a row
     const uint8_t *kp = static_cast<const uint8_t *>(p.k), *vp = static_cast<const uint8_t *>(p.v);
-    uint32_t it = 0, told = 0;  // items (K and V tiles in turn) issued, and reported full
-    auto full_bar = [&](uint32_t i) { return (i & 1) ? &sh.vfull[(i >> 1) & 1] : &sh.kfull[(i >> 1) & 1]; };
-    // Copies that have landed become visible to the tensor cores' reads.
+    uint32_t it = 0;             // items (K and V tiles in turn) issued
+    uint32_t told = 0, pend = 0;  // items reported full, and which of the others are for this warp to report
+    auto full_bar = [&](uint32_t i) { return (i & 1) ? &sh.vfull[(i >> 1) % NS] : &sh.kfull[(i >> 1) % NS]; };
+    // Asynchronous copies that have landed become visible to the tensor cores' reads.
     auto tell = [&](uint32_t upto) {
-      if (told < upto) {
+      if (told < upto && pend) {
         ptx::fence_proxy_async();
         __syncwarp();
-        for (; told < upto; ++told)
-          if (lane == 0) ptx::mbar_arrive(full_bar(told));
+        for (; told < upto; ++told) {
+          if (lane == 0 && ((pend >> (told & 31)) & 1)) ptx::mbar_arrive(full_bar(told));
+          pend &= ~(1u << (told & 31));
+        }
       }
+      told = upto;
     };
     while (walk.next(p)) {
       const int32_t *tab = p.table + (int64_t)walk.r * p.row_pages;
       const int nt = (walk.hi - walk.lo + TT - 1) / TT;
-      auto row_of = [&](int t) -> int64_t {
+      // This lane's token of tile t: page * Hkv + head and the token's place in the page; -1 if it is not there.
+      int ph, place;
+      auto find = [&](int t) {
         const int pos = walk.lo + t * TT + lw * kTokW + lane;
-        if (lane >= kTokW || pos >= walk.hi) return -1;
+        ph = -1;
+        if (lane >= kTokW || t >= nt || pos >= walk.hi) return;
         const int pg = tab[pos / p.page];
-        if (pg < 0 || pg >= p.pages) {
-          set_status(p.status, kStatusPage);
-          return -1;
-        }
-        return (((int64_t)pg * p.Hkv + h) * p.page + pos % p.page) * (D * 2);
+        place = pos % p.page;
+        if (pg < 0 || pg >= p.pages) set_status(p.status, kStatusPage);
+        else ph = pg * p.Hkv + h;
       };
-      int64_t next_row = row_of(0);
+      find(0);
       for (int t = 0; t < nt; ++t) {
-        const int64_t row = next_row;
-        const uint32_t here = __ballot_sync(0xffffffffu, row >= 0);
+        const int cph = ph, cplace = place;
+        const uint32_t here = __ballot_sync(0xffffffffu, cph >= 0);
+        const bool boxes = maps.box && here == (1u << kTokW) - 1u;
+        find(t + 1);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv, ++it) {
-          const uint32_t st = (it >> 1) & 1, n = it >> 2;  // stage, and its uses before
+          const uint32_t st = (it >> 1) % NS, n = (it >> 1) / NS;  // stage, and its uses before
           uint64_t *empty = kv ? &sh.vempty[st] : &sh.kempty[st];
           if (n > 0 && !dead && !__all_sync(0xffffffffu, ptx::mbar_try_wait(empty, (n - 1) & 1))) {
             // Nothing to issue yet: hand over all that is under way first.
-            cp_wait<0>();
-            tell(it);
+            if (pend) {
+              cp_wait<0>();
+              tell(it);
+            }
             wait(empty, (n - 1) & 1, dead);
             dead = __any_sync(0xffffffffu, dead);  // the warp stays together
           }
-          if (kv == 0 && lane == 0) sh.mask[(it >> 1) & 3][lw] = here;
+          if (kv == 0 && lane == 0) sh.mask[(it >> 1) & 7][lw] = here;
           uint8_t *dst = smem + (kv ? C::oV : C::oK) + st * C::kTile;
-          const uint8_t *src = kv ? vp : kp;
-#pragma unroll 8
-          for (int e = 0; e < kTokW * kPer / 32; ++e) {
-            const int at = e * 32 + lane, tk = at / kPer, c = at % kPer;
-            const int64_t off = __shfl_sync(0xffffffffu, row, tk);
-            ptx::cp_async16(dst + (c >> 3) * (TT * 128) + ptx::swz128(lw * kTokW + tk, c & 7),
-                            src + (off < 0 ? 0 : off) + c * 16, off < 0 ? 0 : 16);
+          if (boxes) {
+            const int ph8 = __shfl_sync(0xffffffffu, cph, 8), pl8 = __shfl_sync(0xffffffffu, cplace, 8);
+            if (lane == 0) {
+              ptx::mbar_arrive_expect_tx(full_bar(it), kTokW * D * 2);
+              const CUtensorMap *tm = kv ? &maps.v : &maps.k;
+#pragma unroll
+              for (int a = 0; a < D / 64; ++a) {
+                uint8_t *to = dst + a * (TT * 128) + lw * (kTokW * 128);
+                ptx::tma_load_4d(to, tm, a * 64, 0, cplace, cph, full_bar(it));
+                if (maps.box == 8) ptx::tma_load_4d(to + 8 * 128, tm, a * 64, 0, pl8, ph8, full_bar(it));
+              }
+            }
+          } else {
+            const uint8_t *src = kv ? vp : kp;
+#pragma unroll 4
+            for (int e = 0; e < kTokW * kPer / 32; ++e) {
+              const int at = e * 32 + lane, tk = at / kPer, cc = at % kPer;
+              const int sph = __shfl_sync(0xffffffffu, cph, tk), spl = __shfl_sync(0xffffffffu, cplace, tk);
+              const int64_t off = sph < 0 ? 0 : ((int64_t)sph * p.page + spl) * (D * 2) + cc * 16;
+              ptx::cp_async16(dst + (cc >> 3) * (TT * 128) + ptx::swz128(lw * kTokW + tk, cc & 7), src + off,
+                              sph < 0 ? 0 : 16);
+            }
+            pend |= 1u << (it & 31);
           }
           ptx::cp_async_commit();
-          if (kv == 0) next_row = t + 1 < nt ? row_of(t + 1) : -1;
-          if (it >= 2) {
+          if (pend && it >= 2) {
             cp_wait<2>();
             tell(it - 1);
           }
@@ -330,61 +368,80 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(AttnParam
     }
     cp_wait<0>();
     tell(it);
-  } else if (lane == 0) {
+  } else {
     // ----------------------------------------------------------- products
+    // The whole warp walks along and waits; one elected lane issues.  That
+    // way every descriptor is a warp-uniform value: with the loop itself in
+    // one lane's branch an instruction took about 100 clocks to issue.
     constexpr uint32_t id_s = ptx::idesc_bf16_f32(128, TT);
     constexpr uint32_t id_o = ptx::idesc_bf16_f32(128, D) | ptx::kIdescBMnMajor;
-    uint32_t nq = 0, kt = 0, vt = 0, np[2] = {0, 0}, npv[2] = {0, 0};
+    uint32_t nq = 0, kt = 0, vt = 0;          // Q tiles, K and V tiles used
+    uint32_t cs[2] = {0, 0}, cp[2] = {0, 0};  // jobs of each group: scores issued, products issued
+    const uint64_t qd = ptx::desc_k128(base), kd = ptx::desc_k128(base + C::oK);
+    const uint64_t vd = ptx::desc_mn128(base + C::oV, TT * 128);
     bool work = false;
     while (walk.next(p)) {
-      const int nt = (walk.hi - walk.lo + TT - 1) / TT, nj = nt * kSub;
+      const int nt = __shfl_sync(0xffffffffu, (walk.hi - walk.lo + TT - 1) / TT, 0);
       work = true;
-      wait(&sh.q, nq++ & 1, dead);
-      auto scores = [&](int j) {
-        const int b = j & 1;
-        const bool first = kSub == 1 || b == 0, last = kSub == 1 || b == 1;
-        const uint32_t st = kt & 1;
-        if (first) wait(&sh.kfull[st], (kt >> 1) & 1, dead);
-        // P of this buffer's last job is read once its product is done.
-        if (npv[b] > 0) wait(&sh.pv[b], (npv[b] - 1) & 1, dead);
+      wait_warp(&sh.q, nq++ & 1, dead);
+      // Jobs in the order of issue: job j of the piece is group j % G's, tile
+      // j (kSub = 1) or j / 2 (kSub = 2).
+      const int nj = nt * kSub;
+      auto scores = [&](int g) {
+        const int b = g * 2 + (cs[g] & 1);
+        const bool first = kSub == 1 || g == 0, last = kSub == 1 || g == 1;
+        const uint32_t st = kt % NS;
+        if (first) wait_warp(&sh.kfull[st], (kt / NS) & 1, dead);
+        // The buffer's last weights have been used.
+        if (cs[g] >= 2) wait_warp(&sh.pv[b], ((cs[g] >> 1) - 1) & 1, dead);
         ptx::tc_fence_after();
-        if (!dead) {
-          const uint32_t qa = base + (kSub == 2 ? b * C::kQ : 0), ka = base + C::oK + st * C::kTile;
+        const uint64_t qa = qd + (kSub == 2 ? g * (C::kQ >> 4) : 0), ka = kd + st * (C::kTile >> 4);
+        const uint32_t to = tmem + kSCol + b * TT;
+        if (!dead && ptx::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            ptx::mma_bf16(tmem + kSCol + b * TT, ptx::desc_k128(qa + (kk >> 2) * 16384 + (kk & 3) * 32),
-                          ptx::desc_k128(ka + (kk >> 2) * (TT * 128) + (kk & 3) * 32), id_s, kk > 0);
+            ptx::mma_bf16(to, qa + ((kk >> 2) * 16384 + (kk & 3) * 32) / 16,
+                          ka + ((kk >> 2) * (TT * 128) + (kk & 3) * 32) / 16, id_s, kk > 0);
           ptx::mma_commit(&sh.s[b]);
           if (last) ptx::mma_commit(&sh.kempty[st]);
         }
+        __syncwarp();
+        ++cs[g];
         if (last) ++kt;
       };
-      scores(0);
-      if (nj > 1) scores(1);
-      for (int j = 0; j < nj; ++j) {
-        const int b = j & 1;
-        const bool first = kSub == 1 || b == 0, last = kSub == 1 || b == 1;
-        const uint32_t st = vt & 1;
-        if (first) wait(&sh.vfull[st], (vt >> 1) & 1, dead);
-        wait(&sh.p[b], np[b]++ & 1, dead);
+      auto outputs = [&](int g, bool more) {
+        const int b = g * 2 + (cp[g] & 1);
+        const bool first = kSub == 1 || g == 0, last = kSub == 1 || g == 1;
+        const uint32_t st = vt % NS;
+        if (first) wait_warp(&sh.vfull[st], (vt / NS) & 1, dead);
+        wait_warp(&sh.p[b], (cp[g] >> 1) & 1, dead);
         ptx::tc_fence_after();
-        if (!dead) {
-          const uint32_t va = base + C::oV + st * C::kTile;
-          const uint32_t acc = G == 2 ? j >= 2 : j >= 1;
+        const uint64_t va = vd + st * (C::kTile >> 4);
+        const uint32_t to = tmem + (G == 2 ? g * 128 : 0), from = tmem + kSCol + b * TT;
+        if (!dead && ptx::elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < TT / 16; ++kk)
-            ptx::mma_bf16_ts(tmem + (G == 2 ? b * 128 : 0), tmem + kSCol + b * TT + kk * 8,
-                             ptx::desc_mn128(va + kk * 2048, TT * 128), id_o, acc || kk > 0);
+          for (int kk = 0; kk < TT / 16; ++kk) ptx::mma_bf16_ts(to, from + kk * 8, va + kk * (2048 / 16), id_o, more || kk > 0);
           ptx::mma_commit(&sh.pv[b]);
           if (last) ptx::mma_commit(&sh.vempty[st]);
         }
-        ++npv[b];
+        __syncwarp();
+        ++cp[g];
         if (last) ++vt;
-        if (j + 2 < nj) scores(j + 2);
+      };
+      scores(0);
+      if (G == 2 && nj > 1) scores(1);
+      for (int j = 0; j < nj; j += G) {
+        // A group's next scores go first: they are ready when its exponentials are.
+        if (j + G < nj) scores(0);
+        outputs(0, j > 0);
+        if (G == 2 && j + 1 < nj) {
+          if (j + 3 < nj) scores(1);
+          outputs(1, j > 0);
+        }
       }
     }
     if (work) {
-      ptx::mma_commit(&sh.done);
+      if (ptx::elect_one()) ptx::mma_commit(&sh.done);
       if (!ptx::mbar_wait(&sh.done, 0, kWaitNs)) dead = true;
     }
   }
@@ -401,10 +458,17 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(AttnParam
 template <int D, int kSub>
 cudaError_t run(const AttnParams &p, cudaStream_t s) {
   using C = Cfg<D, kSub>;
-  const cudaError_t e = ensure_smem_limit((const void *)attn_wide<D, kSub>, C::kSmem);
+  cudaError_t e = ensure_smem_limit((const void *)attn_wide<D, kSub>, C::kSmem);
   if (e != cudaSuccess) return e;
+  Maps maps = {};
+  maps.box = p.page % 16 == 0 ? 16 : (p.page % 8 == 0 ? 8 : 0);
+  // Coordinates are 32-bit.
+  if ((long long)p.pages * p.Hkv > 0x7fffffffLL) maps.box = 0;
+  if (maps.box && (!encode_rows(&maps.k, p.k, D, 1, p.page, p.pages * p.Hkv, maps.box) ||
+                   !encode_rows(&maps.v, p.v, D, 1, p.page, p.pages * p.Hkv, maps.box)))
+    return cudaErrorInvalidValue;
   return launch_kernel(attn_wide<D, kSub>, (unsigned)((long long)p.parts * p.Hkv * p.row_tiles), C::kThreads, C::kSmem,
-                       false, s, p);
+                       false, s, p, maps);
 }
 
 }  // namespace
