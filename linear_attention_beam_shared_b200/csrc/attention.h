@@ -112,17 +112,28 @@ struct PlanWalk {
       base = 0;
       return;
     }
+    slot = c;
+    if (p.R <= 32) {
+      // Each warp for itself: lane = request, no barrier.
+      const int lane = threadIdx.x & 31, mine = lane < p.R ? tiles_of(p, lane) : 0;
+      long long incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      const long long total = __shfl_sync(0xffffffffu, incl, 31);
+      if (!share(c, total, p.parts)) return;
+      // The first request that ends behind the part's first tile.
+      r = __ffs(__ballot_sync(0xffffffffu, incl > at)) - 1;
+      base = __shfl_sync(0xffffffffu, incl - mine, r);
+      slot += --r;
+      return;
+    }
     int r0, r1;
     long long before;
     const long long total = plan_scan<kThreads>(p, sm, r0, r1, before);
-    const long long n = total < p.parts ? total : p.parts;
-    if (c >= n) {
-      at = end = 0;
-      return;
-    }
-    at = c * total / n;
-    end = (c + 1) * total / n;
-    slot = c;
+    if (!share(c, total, p.parts)) return;
     for (int q = r0; q < r1; ++q) {
       const int t = tiles_of(p, q);
       if (at >= before && at < before + t) {  // exactly one thread and request
@@ -134,7 +145,21 @@ struct PlanWalk {
     __syncthreads();
     r = sm.r - 1;
     base = sm.base;
-    slot = c + r;
+    slot += r;
+  }
+  // Part c's tiles; false if there are none.
+  __device__ __forceinline__ bool share(int c, long long total, int parts) {
+    const long long n = total < parts ? total : parts;
+    at = end = 0;
+    if (c >= n) return false;
+    if (total < (1LL << 18)) {  // 32-bit division is several times shorter; at most 4736 parts
+      at = (uint32_t)c * (uint32_t)total / (uint32_t)n;
+      end = ((uint32_t)c + 1u) * (uint32_t)total / (uint32_t)n;
+    } else {
+      at = c * total / n;
+      end = (c + 1) * total / n;
+    }
+    return true;
   }
   __device__ __forceinline__ bool next(const AttnParams &p) {
     if (at >= end) return false;
@@ -162,9 +187,41 @@ struct PlanWalk {
   }
 };
 
+// The slots of request r, whose t tiles start at `first`: tile x lies in part
+// ((x + 1) n - 1) / total.
+__device__ __forceinline__ void slots_of(long long first, int t, long long total, int parts, int r, int &off, int &pieces) {
+  if (t == 0) {
+    off = pieces = 0;
+    return;
+  }
+  const long long n = total < parts ? total : parts;
+  long long c0, c1;
+  if (total < (1LL << 18)) {
+    c0 = ((uint32_t)(first + 1) * (uint32_t)n - 1u) / (uint32_t)total;
+    c1 = ((uint32_t)(first + t) * (uint32_t)n - 1u) / (uint32_t)total;
+  } else {
+    c0 = ((first + 1) * n - 1) / total;
+    c1 = ((first + t) * n - 1) / total;
+  }
+  off = (int)c0 + r;
+  pieces = (int)(c1 - c0) + 1;
+}
+
 // Request r: its first slot and how many it has.
 template <int kThreads>
 __device__ __forceinline__ void plan_row(const AttnParams &p, PlanSmem &sm, int r, int &off, int &pieces) {
+  if (p.R <= 32) {
+    const int lane = threadIdx.x & 31, mine = lane < p.R ? tiles_of(p, lane) : 0;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    const int t = __shfl_sync(0xffffffffu, mine, r);
+    slots_of(__shfl_sync(0xffffffffu, incl, r) - t, t, __shfl_sync(0xffffffffu, incl, 31), p.parts, r, off, pieces);
+    return;
+  }
   int r0, r1;
   long long before;
   const long long total = plan_scan<kThreads>(p, sm, r0, r1, before);
@@ -173,14 +230,7 @@ __device__ __forceinline__ void plan_row(const AttnParams &p, PlanSmem &sm, int 
     sm.base = before;
   }
   __syncthreads();
-  const long long first = sm.base, n = total < p.parts ? total : p.parts, t = tiles_of(p, r);
-  if (t == 0) {
-    off = pieces = 0;
-    return;
-  }
-  const long long c0 = ((first + 1) * n - 1) / total, c1 = ((first + t) * n - 1) / total;
-  off = (int)c0 + r;
-  pieces = (int)(c1 - c0) + 1;
+  slots_of(sm.base, tiles_of(p, r), total, p.parts, r, off, pieces);
 }
 
 // Partial results of row m of (slot, head).

@@ -31,8 +31,7 @@
 // page table into rings of K and V tiles: by TMA boxes of 16 or 8 tokens
 // where all of a warp's tokens are there and pages are multiples of 8 tokens,
 // otherwise by 16-byte asynchronous copies, zeros for tokens that are not
-// there.  (Those alone held the SM to 18 bytes a clock.)  One thread issues
-// the products.  Every wait is bounded: one that runs out sets
+// there.  (Those alone held the SM to 18 bytes a clock.)  Every wait is bounded: one that runs out sets
 // ONELA_STATUS_TIMEOUT and the results become NaN.
 #include "attention.h"
 
@@ -54,11 +53,12 @@ template <int D, int kSub>
 struct Cfg {
   static constexpr int G = D == 256 ? 1 : 2;  // softmax groups
   static constexpr int kSoft = G * 128;
-  static constexpr int kThreads = kSoft + 128 + 32;
+  static constexpr int kThreads = kSoft + 128 + 64;
   static constexpr int kStages = D == 256 ? 2 : 4;
   static constexpr int kQ = 128 * D * 2;    // bytes of 128 Q rows
   static constexpr int kTile = TT * D * 2;  // bytes of a K or V tile
-  static constexpr int oK = kSub * kQ, oV = oK + kStages * kTile, oEnd = oV + kStages * kTile;
+  static constexpr int oK = kSub * kQ, oV = oK + kStages * kTile, oOut = oV + kStages * kTile;
+  static constexpr int oEnd = oOut + kSoft / 32 * 4096;  // 32 rows x 32 columns of O for each softmax warp
   // Above half of an SM's shared memory, so that one CTA has the SM (and its
   // tensor memory) for itself.
   static constexpr int kSmem = oEnd + 1024 < 120 * 1024 ? 120 * 1024 : oEnd + 1024;
@@ -67,7 +67,7 @@ struct Cfg {
 struct Shared {
   uint64_t kfull[4], kempty[4], vfull[4], vempty[4];
   uint64_t s[4], p[4], pv[4];  // by group and score buffer
-  uint64_t q, done;
+  uint64_t q, done[2];
   uint32_t tmem;
   uint32_t mask[8][4];  // by tile (ring of 8) and load warp: the 16 tokens that are there
   PlanSmem plan;
@@ -130,7 +130,8 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
       ptx::mbar_init(&sh.pv[i], 1);
     }
     ptx::mbar_init(&sh.q, C::kSoft);
-    ptx::mbar_init(&sh.done, 1);
+    ptx::mbar_init(&sh.done[0], 1);
+    ptx::mbar_init(&sh.done[1], 1);
     ptx::mbar_fence_init();
   }
   if (warp == kMmaWarp) {
@@ -164,14 +165,13 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
         // A warp brings its 32 rows, 32 16-byte chunks at a time.
         uint8_t *qd = smem + (kSub == 2 ? grp * C::kQ : 0);
         constexpr int kPer = D / 8;
+        const int64_t mine = m < p.M ? ((int64_t)r * p.W + m / p.G) * p.q_stride + (int64_t)(h * p.G + m % p.G) * D : -1;
 #pragma unroll 8
         for (int e = 0; e < kPer; ++e) {
-          const int at = e * 32 + lane, rw = (warp & 3) * 32 + at / kPer, cc = at % kPer, mm = m1 + rw;
+          const int rl = (e * 32 + lane) / kPer, cc = (e * 32 + lane) % kPer, rw = (warp & 3) * 32 + rl;
+          const int64_t at = __shfl_sync(0xffffffffu, mine, rl);
           uint4 x = make_uint4(0, 0, 0, 0);
-          if (mm < p.M)
-            x = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) +
-                                                      ((int64_t)r * p.W + mm / p.G) * p.q_stride +
-                                                      (int64_t)(h * p.G + mm % p.G) * D) + cc);
+          if (at >= 0) x = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + at) + cc);
           *reinterpret_cast<uint4 *>(qd + (cc >> 3) * 16384 + ptx::swz128(rw, cc & 7)) = x;
         }
       }
@@ -255,25 +255,32 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
         wait_warp(&sh.pv[grp * 2 + ((c - 1) & 1)], ((c - 1) >> 1) & 1, dead);
         ptx::tc_fence_after();
       }
+      // Rows go out 128 bytes at a time: 32 columns of the warp's 32 rows through shared memory.
+      uint8_t *stage = smem + C::oOut + warp * 4096;
 #pragma unroll 1
       for (int e = 0; e < D / 32; ++e) {
         float z[32];
         if (any) {
           ptx::tmem_ld32(o_t + e * 32, z);
           ptx::tmem_ld_wait();
-        }
-        if (m < p.M) {
-          float *out = p.part_o + pr * D + e * 32;
+        } else {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            float y[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) y[q] = any ? z[i + q] : 0.f;
-            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + i), "f"(y[0]), "f"(y[1]),
-                         "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7])
-                         : "memory");
-          }
+          for (int i = 0; i < 32; ++i) z[i] = 0.f;
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<float4 *>(stage + ptx::swz128(lane, i)) =
+              make_float4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]);
+        __syncwarp();
+        float *out = p.part_o + (pr - lane) * D + e * 32;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rl = i * 4 + (lane >> 3);
+          if (m - lane + rl < p.M)
+            *reinterpret_cast<float4 *>(out + (int64_t)rl * D + (lane & 7) * 4) =
+                *reinterpret_cast<const float4 *>(stage + ptx::swz128(rl, lane & 7));
+        }
+        __syncwarp();
       }
       if (any) ptx::tc_fence_before();
       if (m < p.M) p.part_ml[pr] = dead ? make_float2(0.f, CUDART_NAN_F) : make_float2(mref, sum);
@@ -370,79 +377,70 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
     tell(it);
   } else {
     // ----------------------------------------------------------- products
-    // The whole warp walks along and waits; one elected lane issues.  That
-    // way every descriptor is a warp-uniform value: with the loop itself in
-    // one lane's branch an instruction took about 100 clocks to issue.
+    // One warp issues the scores and one the outputs, so that the waits of
+    // one lie under the products of the other; barriers order them.  The
+    // whole warp walks along and waits and one elected lane issues: that way every
+    // descriptor is a warp-uniform value (with the loop itself in one lane's
+    // branch an instruction took about 100 clocks to issue).
+    const bool is_s = warp == kMmaWarp;
     constexpr uint32_t id_s = ptx::idesc_bf16_f32(128, TT);
     constexpr uint32_t id_o = ptx::idesc_bf16_f32(128, D) | ptx::kIdescBMnMajor;
-    uint32_t nq = 0, kt = 0, vt = 0;          // Q tiles, K and V tiles used
-    uint32_t cs[2] = {0, 0}, cp[2] = {0, 0};  // jobs of each group: scores issued, products issued
     const uint64_t qd = ptx::desc_k128(base), kd = ptx::desc_k128(base + C::oK);
     const uint64_t vd = ptx::desc_mn128(base + C::oV, TT * 128);
-    bool work = false;
+    uint32_t nq = 0, tiles = 0;   // Q tiles, K or V tiles used
+    uint32_t c[2] = {0, 0};       // jobs of each group so far
     while (walk.next(p)) {
       const int nt = __shfl_sync(0xffffffffu, (walk.hi - walk.lo + TT - 1) / TT, 0);
-      work = true;
-      wait_warp(&sh.q, nq++ & 1, dead);
       // Jobs in the order of issue: job j of the piece is group j % G's, tile
       // j (kSub = 1) or j / 2 (kSub = 2).
       const int nj = nt * kSub;
-      auto scores = [&](int g) {
-        const int b = g * 2 + (cs[g] & 1);
-        const bool first = kSub == 1 || g == 0, last = kSub == 1 || g == 1;
-        const uint32_t st = kt % NS;
-        if (first) wait_warp(&sh.kfull[st], (kt / NS) & 1, dead);
-        // The buffer's last weights have been used.
-        if (cs[g] >= 2) wait_warp(&sh.pv[b], ((cs[g] >> 1) - 1) & 1, dead);
-        ptx::tc_fence_after();
-        const uint64_t qa = qd + (kSub == 2 ? g * (C::kQ >> 4) : 0), ka = kd + st * (C::kTile >> 4);
-        const uint32_t to = tmem + kSCol + b * TT;
-        if (!dead && ptx::elect_one()) {
+      if (is_s) wait_warp(&sh.q, nq & 1, dead);
+      ++nq;
+      for (int j0 = 0; j0 < nj; j0 += G) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            ptx::mma_bf16(to, qa + ((kk >> 2) * 16384 + (kk & 3) * 32) / 16,
-                          ka + ((kk >> 2) * (TT * 128) + (kk & 3) * 32) / 16, id_s, kk > 0);
-          ptx::mma_commit(&sh.s[b]);
-          if (last) ptx::mma_commit(&sh.kempty[st]);
-        }
-        __syncwarp();
-        ++cs[g];
-        if (last) ++kt;
-      };
-      auto outputs = [&](int g, bool more) {
-        const int b = g * 2 + (cp[g] & 1);
-        const bool first = kSub == 1 || g == 0, last = kSub == 1 || g == 1;
-        const uint32_t st = vt % NS;
-        if (first) wait_warp(&sh.vfull[st], (vt / NS) & 1, dead);
-        wait_warp(&sh.p[b], (cp[g] >> 1) & 1, dead);
-        ptx::tc_fence_after();
-        const uint64_t va = vd + st * (C::kTile >> 4);
-        const uint32_t to = tmem + (G == 2 ? g * 128 : 0), from = tmem + kSCol + b * TT;
-        if (!dead && ptx::elect_one()) {
+        for (int g = 0; g < G; ++g) {
+          if (j0 + g >= nj) break;
+          const uint32_t cg = c[g]++;
+          const int b = g * 2 + (cg & 1);
+          const bool first = kSub == 1 || g == 0, last = kSub == 1 || g == 1;
+          const uint32_t st = tiles % NS, turn = tiles / NS;
+          if (last) ++tiles;
+          if (is_s) {
+            if (first) wait_warp(&sh.kfull[st], turn & 1, dead);
+            // The weights that were in this buffer have been used.
+            if (cg >= 2) wait_warp(&sh.pv[b], ((cg >> 1) - 1) & 1, dead);
+            ptx::tc_fence_after();
+            const uint64_t qa = qd + (kSub == 2 ? g * (C::kQ >> 4) : 0), ka = kd + st * (C::kTile >> 4);
+            const uint32_t to = tmem + kSCol + b * TT;
+            if (!dead && ptx::elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < TT / 16; ++kk) ptx::mma_bf16_ts(to, from + kk * 8, va + kk * (2048 / 16), id_o, more || kk > 0);
-          ptx::mma_commit(&sh.pv[b]);
-          if (last) ptx::mma_commit(&sh.vempty[st]);
-        }
-        __syncwarp();
-        ++cp[g];
-        if (last) ++vt;
-      };
-      scores(0);
-      if (G == 2 && nj > 1) scores(1);
-      for (int j = 0; j < nj; j += G) {
-        // A group's next scores go first: they are ready when its exponentials are.
-        if (j + G < nj) scores(0);
-        outputs(0, j > 0);
-        if (G == 2 && j + 1 < nj) {
-          if (j + 3 < nj) scores(1);
-          outputs(1, j > 0);
+              for (int kk = 0; kk < D / 16; ++kk)
+                ptx::mma_bf16(to, qa + ((kk >> 2) * 16384 + (kk & 3) * 32) / 16,
+                              ka + ((kk >> 2) * (TT * 128) + (kk & 3) * 32) / 16, id_s, kk > 0);
+              ptx::mma_commit(&sh.s[b]);
+              if (last) ptx::mma_commit(&sh.kempty[st]);
+            }
+          } else {
+            if (first) wait_warp(&sh.vfull[st], turn & 1, dead);
+            wait_warp(&sh.p[b], (cg >> 1) & 1, dead);
+            ptx::tc_fence_after();
+            const uint64_t va = vd + st * (C::kTile >> 4);
+            const uint32_t to = tmem + (G == 2 ? g * 128 : 0), from = tmem + kSCol + b * TT;
+            if (!dead && ptx::elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < TT / 16; ++kk)
+                ptx::mma_bf16_ts(to, from + kk * 8, va + kk * (2048 / 16), id_o, j0 > 0 || kk > 0);
+              ptx::mma_commit(&sh.pv[b]);
+              if (last) ptx::mma_commit(&sh.vempty[st]);
+            }
+          }
+          __syncwarp();
         }
       }
     }
-    if (work) {
-      if (ptx::elect_one()) ptx::mma_commit(&sh.done);
-      if (!ptx::mbar_wait(&sh.done, 0, kWaitNs)) dead = true;
+    if (nq > 0) {
+      if (ptx::elect_one()) ptx::mma_commit(&sh.done[is_s]);
+      if (!ptx::mbar_wait(&sh.done[is_s], 0, kWaitNs)) dead = true;
     }
   }
   if (dead) set_status(p.status, ONELA_STATUS_TIMEOUT);
