@@ -292,29 +292,34 @@ __global__ void __launch_bounds__(kWpr == 1 ? 128 : kWpr * 32) attn_join(AttnPar
     const int n = given < 0 ? 0 : (given > bcap ? bcap : given);
     if (n != given && lane == 0) set_status(p.status, kStatusLength);
     const int32_t *tab = p.btable + ((int64_t)r * p.W + w) * p.brow_pages;
-    for (int t0 = 4 * part; t0 < n; t0 += 4 * kWpr) {
-      float s[4], vv[4][N];
+    // The table's entries 32 tokens at a time, one per lane, as element
+    // offsets of the rows (-1: not there); then K and V rows four at a time.
+    for (int tb = 0; tb < n; tb += 32) {
+    int64_t where = -1;
+    if (tb + lane < n) {
+      const int pg = tab[(tb + lane) / p.bpage];
+      if (pg >= 0 && pg < p.bpages) where = (((int64_t)pg * p.Hkv + h) * p.bpage + (tb + lane) % p.bpage) * p.d;
+      else set_status(p.status, kStatusPage);
+    }
+    const int nb = min(32, n - tb);
+    for (int t0 = 4 * part; t0 < nb; t0 += 4 * kWpr) {
+      float s[4], kk[4][N], vv[4][N];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int t = t0 + j;
-        s[j] = -CUDART_INF_F;
+        const int64_t at = __shfl_sync(0xffffffffu, where, t0 + j);
+        s[j] = at >= 0 ? 0.f : -CUDART_INF_F;
+        if (at >= 0) {
+          C::load(bk + at, lane, p.d, kk[j]);
+          C::load(bv + at, lane, p.d, vv[j]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) vv[j][i] = 0.f;
-        if (t < n) {
-          const int pg = tab[t / p.bpage];
-          if (pg >= 0 && pg < p.bpages) {
-            const int64_t at = (((int64_t)pg * p.Hkv + h) * p.bpage + t % p.bpage) * p.d;
-            float kk[N];
-            C::load(bk + at, lane, p.d, kk);
-            C::load(bv + at, lane, p.d, vv[j]);
-            s[j] = 0.f;
-#pragma unroll
-            for (int i = 0; i < N; ++i) s[j] += qv[i] * kk[i];
-          } else if (lane == 0) {
-            set_status(p.status, kStatusPage);
-          }
+          for (int i = 0; i < N; ++i) kk[j][i] = vv[j][i] = 0.f;
         }
       }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[j] += qv[i] * kk[j][i];
       float top = mx;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -334,6 +339,7 @@ __global__ void __launch_bounds__(kWpr == 1 ? 128 : kWpr * 32) attn_join(AttnPar
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[i] += e * vv[j][i];
       }
+    }
     }
   }
   ptx::pdl_wait();
@@ -419,10 +425,9 @@ bool tc_fits(const onela_attention_config &c, const AttnParams &p) {
   return c.dtype == ONELA_BF16 && (c.d == 64 || c.d == 128 || c.d == 256) && c.q_stride % 8 == 0 && (at & 15) == 0;
 }
 
-AttnKind choose(const onela_attention_config &c, const AttnParams &p, bool want_mass) {
+AttnKind choose(const onela_attention_config &c, const AttnParams &p) {
   if (c.kernel == ONELA_KERNEL_SIMT || !tc_fits(c, p)) return kAttnSimt;
-  if (p.M <= 16) return kAttnNarrow;
-  return want_mass ? kAttnSimt : kAttnWide;
+  return p.M <= 16 ? kAttnNarrow : kAttnWide;
 }
 
 // Chooses the division and lays out the scratch; the bytes needed.
@@ -443,7 +448,7 @@ size_t plan_call(const onela_attention_config &c, bool want_mass, AttnParams &p,
   p.brow_pages = c.beam_row_pages;
   p.q_stride = c.q_stride;
   p.scale_log2 = c.scale * kLog2e;
-  const AttnKind kind = choose(c, p, want_mass);
+  const AttnKind kind = choose(c, p);
   int ctas = 4 * kAttnSMs;  // that run at once
   p.rows = kRows;
   p.tile = kToks;
@@ -489,7 +494,7 @@ size_t plan_call(const onela_attention_config &c, bool want_mass, AttnParams &p,
   }
   if (want_mass) {
     p.lse2 = reinterpret_cast<float *>(take((size_t)p.R * p.Hkv * p.M * 4));
-    p.scores = reinterpret_cast<float *>(take((size_t)p.R * p.Hkv * p.M * p.cap * 4));
+    if (kind != kAttnWide) p.scores = reinterpret_cast<float *>(take((size_t)p.R * p.Hkv * p.M * p.cap * 4));
   }
   used = kind;
   return at;
@@ -540,6 +545,7 @@ cudaError_t run(const AttnParams &p, AttnKind kind, bool vec, cudaStream_t s) {
 
   e = run_join<T>(p, s);
   if (e != cudaSuccess || !p.mass_out) return e;
+  if (kind == kAttnWide) return launch_attn_mass_wide(p, s);
   return launch_kernel(attn_mass, (unsigned)((long long)p.R * p.Hkv * ((p.cap + kThreads - 1) / kThreads)), kThreads, 0, true,
                 s, p);
 }

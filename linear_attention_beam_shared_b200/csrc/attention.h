@@ -260,6 +260,7 @@ __device__ __forceinline__ void set_status(int32_t *status, int32_t bit) {
 enum AttnKind { kAttnSimt = 0, kAttnNarrow = 1, kAttnWide = 2 };
 cudaError_t launch_attn_narrow(const AttnParams &p, cudaStream_t s);  // attention_narrow.cu
 cudaError_t launch_attn_wide(const AttnParams &p, cudaStream_t s);    // attention_wide.cu
+cudaError_t launch_attn_mass_wide(const AttnParams &p, cudaStream_t s);
 
 template <typename... P, typename... A>
 cudaError_t launch_kernel(void (*f)(P...), unsigned grid, unsigned threads, size_t smem, bool pdl, cudaStream_t s, A... a) {

@@ -58,7 +58,9 @@ struct Cfg {
   static constexpr int kQ = 128 * D * 2;    // bytes of 128 Q rows
   static constexpr int kTile = TT * D * 2;  // bytes of a K or V tile
   static constexpr int oK = kSub * kQ, oV = oK + kStages * kTile, oOut = oV + kStages * kTile;
-  static constexpr int oEnd = oOut + kSoft / 32 * 4096;  // 32 rows x 32 columns of O for each softmax warp
+  // 32 rows x 32 columns of O for each softmax warp, on their way out: over
+  // the group's own Q rows (kSub = 2), else in a place of its own, for the other group may still read Q.
+  static constexpr int oEnd = oOut + (kSub == 2 ? 0 : kSoft / 32 * 4096);
   // Above half of an SM's shared memory, so that one CTA has the SM (and its
   // tensor memory) for itself.
   static constexpr int kSmem = oEnd + 1024 < 120 * 1024 ? 120 * 1024 : oEnd + 1024;
@@ -256,7 +258,7 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
         ptx::tc_fence_after();
       }
       // Rows go out 128 bytes at a time: 32 columns of the warp's 32 rows through shared memory.
-      uint8_t *stage = smem + C::oOut + warp * 4096;
+      uint8_t *stage = smem + (kSub == 2 ? grp * C::kQ + (warp & 3) * 4096 : C::oOut + warp * 4096);
 #pragma unroll 1
       for (int e = 0; e < D / 32; ++e) {
         float z[32];
@@ -453,6 +455,191 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
   }
 }
 
+// ---------------------------------------------------------------------------
+// The weight each prompt position drew, once every row's lse is known: the
+// scores again, this time transposed, S^T = K Q^T, so that a thread owns a
+// token and adds exp2(s - lse2) over the rows in order (no atomics, one writer
+// per position).  Recomputing costs half of the attention's products; keeping
+// the scores would cost 4 bytes a row and token, more than K and V themselves
+// from 64 rows on at d = 64.  One CTA per (request, head, 128 tokens): K is an operand
+// held in shared memory, tiles of 64 rows of Q pass through a ring, two groups of four
+// warps take them in turn.
+template <int D>
+struct MassCfg {
+  static constexpr int kStages = 4;
+  static constexpr int kK = 128 * D * 2, kTile = 64 * D * 2;
+  static constexpr int kThreads = 256 + 128 + 32;
+  static constexpr int kSmem = kK + kStages * kTile + 1024;
+};
+
+struct MassShared {
+  uint64_t k, full[4], empty[4], s[4], sfree[4], done;
+  uint32_t tmem;
+  float lse2[4][64];  // by Q stage
+  float sums[128];
+};
+
+template <int D>
+__global__ void __launch_bounds__(MassCfg<D>::kThreads, 1) attn_mass_wide(const __grid_constant__ AttnParams p) {
+  using C = MassCfg<D>;
+  constexpr int NS = C::kStages;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ MassShared sh;
+  uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t base = ptx::smem_u32(smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int chunks = (p.cap + 127) / 128;
+  const int t0 = (int)(blockIdx.x % chunks) * 128, rh = blockIdx.x / chunks, r = rh / p.Hkv, h = rh % p.Hkv;
+  const int len = prompt_len(p, r);
+  if (t0 >= len) return;
+  const int nt = (p.M + 63) / 64;  // tiles of Q rows
+
+  if (tid == 0) {
+    ptx::mbar_init(&sh.k, 128);
+    for (int i = 0; i < 4; ++i) {
+      ptx::mbar_init(&sh.full[i], 128);
+      ptx::mbar_init(&sh.empty[i], 128);  // by the threads that took the stage's tile: its product is done by then
+      ptx::mbar_init(&sh.s[i], 1);
+      ptx::mbar_init(&sh.sfree[i], 128);
+    }
+    ptx::mbar_init(&sh.done, 1);
+    ptx::mbar_fence_init();
+  }
+  if (warp == 12) {
+    ptx::tmem_alloc(&sh.tmem, 256);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
+  bool dead = false;
+
+  if (warp < 8) {
+    // ----------------------------------------------------- thread = token
+    const int grp = warp >> 2, tok = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    float sum = 0.f;
+    uint32_t c = 0;
+    for (int t = grp; t < nt; t += 2, ++c) {
+      const int b = grp * 2 + (c & 1), st = t % NS;
+      wait_warp(&sh.s[b], (c >> 1) & 1, dead);
+      ptx::tc_fence_after();
+      float x[2][32];
+      ptx::tmem_ld32(tmem + lanes + b * 64, x[0]);
+      ptx::tmem_ld32(tmem + lanes + b * 64 + 32, x[1]);
+      ptx::tmem_ld_wait();
+      float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 64; ++i) a[i & 3] += ex2(fmaf(x[i >> 5][i & 31], p.scale_log2, -sh.lse2[st][i]));
+      sum += (a[0] + a[1]) + (a[2] + a[3]);
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(&sh.sfree[b]);
+      ptx::mbar_arrive(&sh.empty[st]);
+    }
+    if (grp == 1) sh.sums[tok] = sum;
+    ptx::bar_sync(1, 256);
+    if (grp == 0 && t0 + tok < len) {
+      const int64_t at = (int64_t)rh * p.cap + t0 + tok;
+      // A position on a bad page (its zeros gave scores of 0) draws nothing.
+      const int pg = p.table[(int64_t)r * p.row_pages + (t0 + tok) / p.page];
+      const float drawn = dead ? CUDART_NAN_F : (pg >= 0 && pg < p.pages ? sum + sh.sums[tok] : 0.f);
+      p.mass_out[at] = p.mass ? p.mass[at] + drawn : drawn;
+    }
+  } else if (warp < 12) {
+    // -------------------------------------------------------------- loads
+    const int lw = warp - 8, lt = tid - 256;
+    constexpr int kPer = D * 2 / 16;
+    {
+      // K rows of this warp's 32 tokens, zeros for those that are not there.
+      const int pos = t0 + lw * 32 + lane;
+      int64_t mine = -1;
+      if (pos < len) {
+        const int pg = p.table[(int64_t)r * p.row_pages + pos / p.page];
+        if (pg >= 0 && pg < p.pages) mine = (((int64_t)pg * p.Hkv + h) * p.page + pos % p.page) * (D * 2);
+      }
+#pragma unroll 4
+      for (int e = 0; e < kPer; ++e) {
+        const int rl = (e * 32 + lane) / kPer, cc = (e * 32 + lane) % kPer;
+        const int64_t at = __shfl_sync(0xffffffffu, mine, rl);
+        ptx::cp_async16(smem + (cc >> 3) * 16384 + ptx::swz128(lw * 32 + rl, cc & 7),
+                        static_cast<const uint8_t *>(p.k) + (at < 0 ? 0 : at + cc * 16), at < 0 ? 0 : 16);
+      }
+      ptx::cp_async_commit();
+    }
+    auto tell = [&](int t) {  // tile t has landed
+      ptx::fence_proxy_async();
+      ptx::mbar_arrive(&sh.full[t % NS]);
+    };
+    for (int t = 0; t < nt; ++t) {
+      const int st = t % NS;
+      if (t >= NS) wait_warp(&sh.empty[st], (t / NS - 1) & 1, dead);
+      dead = __any_sync(0xffffffffu, dead);
+      uint8_t *dst = smem + C::kK + st * C::kTile;
+      const int m = t * 64 + lw * 16 + lane;  // lanes 0 .. 15: this warp's rows
+      const int64_t mine = lane < 16 && m < p.M
+                               ? (((int64_t)r * p.W + m / p.G) * p.q_stride + (int64_t)(h * p.G + m % p.G) * D) * 2
+                               : -1;
+#pragma unroll 4
+      for (int e = 0; e < kPer / 2; ++e) {
+        const int rl = (e * 32 + lane) / kPer, cc = (e * 32 + lane) % kPer;
+        const int64_t at = __shfl_sync(0xffffffffu, mine, rl);
+        ptx::cp_async16(dst + (cc >> 3) * 8192 + ptx::swz128(lw * 16 + rl, cc & 7),
+                        static_cast<const uint8_t *>(p.q) + (at < 0 ? 0 : at + cc * 16), at < 0 ? 0 : 16);
+      }
+      ptx::cp_async_commit();
+      if (t == 0) ptx::pdl_wait();  // the lse of every row is the join's
+      if (lt < 64) {
+        // A row that is not there, or drew nothing, adds exp2(-inf) = 0.
+        const int mm = t * 64 + lt;
+        const float l = mm < p.M ? p.lse2[(int64_t)rh * p.M + mm] : -CUDART_INF_F;
+        sh.lse2[st][lt] = l == -CUDART_INF_F ? CUDART_INF_F : l;
+      }
+      if (t == 0) {
+        cp_wait<1>();
+        ptx::fence_proxy_async();
+        ptx::mbar_arrive(&sh.k);
+      }
+      if (t >= 1) {
+        cp_wait<1>();
+        tell(t - 1);
+      }
+    }
+    cp_wait<0>();
+    tell(nt - 1);
+  } else {
+    // ----------------------------------------------------------- products
+    constexpr uint32_t id = ptx::idesc_bf16_f32(128, 64);
+    const uint64_t kd = ptx::desc_k128(base), qd = ptx::desc_k128(base + C::kK);
+    wait_warp(&sh.k, 0, dead);
+    for (int t = 0; t < nt; ++t) {
+      const int g = t & 1, n = t >> 1, b = g * 2 + (n & 1), st = t % NS;
+      wait_warp(&sh.full[st], (t / NS) & 1, dead);
+      if (n >= 2) wait_warp(&sh.sfree[b], ((n >> 1) - 1) & 1, dead);
+      ptx::tc_fence_after();
+      const uint64_t qa = qd + st * (C::kTile >> 4);
+      if (!dead && ptx::elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          ptx::mma_bf16(tmem + b * 64, kd + ((kk >> 2) * 16384 + (kk & 3) * 32) / 16,
+                        qa + ((kk >> 2) * 8192 + (kk & 3) * 32) / 16, id, kk > 0);
+        ptx::mma_commit(&sh.s[b]);
+      }
+      __syncwarp();
+    }
+    if (ptx::elect_one()) ptx::mma_commit(&sh.done);
+    if (!ptx::mbar_wait(&sh.done, 0, kWaitNs)) dead = true;
+  }
+  if (dead) set_status(p.status, ONELA_STATUS_TIMEOUT);
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 256);
+  }
+}
+
 template <int D, int kSub>
 cudaError_t run(const AttnParams &p, cudaStream_t s) {
   using C = Cfg<D, kSub>;
@@ -476,6 +663,19 @@ cudaError_t launch_attn_wide(const AttnParams &p, cudaStream_t s) {
   if (p.d == 64) return two ? run<64, 2>(p, s) : run<64, 1>(p, s);
   if (p.d == 128) return two ? run<128, 2>(p, s) : run<128, 1>(p, s);
   return run<256, 1>(p, s);
+}
+
+template <int D>
+static cudaError_t run_mass(const AttnParams &p, cudaStream_t s) {
+  const cudaError_t e = ensure_smem_limit((const void *)attn_mass_wide<D>, MassCfg<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(attn_mass_wide<D>, (unsigned)((long long)p.R * p.Hkv * ((p.cap + 127) / 128)),
+                       MassCfg<D>::kThreads, MassCfg<D>::kSmem, true, s, p);
+}
+
+cudaError_t launch_attn_mass_wide(const AttnParams &p, cudaStream_t s) {
+  if (p.d == 64) return run_mass<64>(p, s);
+  return p.d == 128 ? run_mass<128>(p, s) : run_mass<256>(p, s);
 }
 
 }  // namespace onela
