@@ -10,11 +10,15 @@
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
+#include <algorithm>
+
 #include "../../include/onela.h"
 #include "internal.h"
 
 namespace onela {
 namespace {
+
+constexpr int kSMs = 148;
 
 __device__ __forceinline__ float ld(const void *p, int64_t i, int bf16) {
   return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]) : static_cast<const float *>(p)[i];
@@ -24,159 +28,238 @@ __device__ __forceinline__ void st(void *p, int64_t i, float x, int bf16) {
   else static_cast<float *>(p)[i] = x;
 }
 
-// Eight consecutive elements as floats; 16-byte aligned rows.
-__device__ __forceinline__ void ld8(const void *p, int64_t i, int bf16, float (&v)[8]) {
-  if (bf16) {
-    union { uint4 u; __nv_bfloat162 h[4]; } a;
-    a.u = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p) + i);
+// Eight consecutive elements, 16-byte aligned, as they lie in memory and as floats.
+template <bool kBf>
+struct Vec;
+template <>
+struct Vec<true> {
+  uint4 u;
+  __device__ __forceinline__ void load(const void *p, int64_t i) {
+    u = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p) + i));
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float2 f = __bfloat1622float2(a.h[e]);
-      v[2 * e] = f.x;
-      v[2 * e + 1] = f.y;
+      v[2 * e] = __uint_as_float(w[e] << 16);
+      v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
     }
-  } else {
-    const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-    const float4 a = q[0], b = q[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   }
-}
-__device__ __forceinline__ void st8(void *p, int64_t i, int bf16, const float (&v)[8]) {
-  if (bf16) {
+  static __device__ __forceinline__ void store(void *p, int64_t i, const float (&v)[8]) {
     union { uint4 u; __nv_bfloat162 h[4]; } a;
 #pragma unroll
     for (int e = 0; e < 4; ++e) a.h[e] = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
     *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p) + i) = a.u;
-  } else {
+  }
+};
+template <>
+struct Vec<false> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const void *p, int64_t i) {
+    const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+    a = __ldcs(q);
+    b = __ldcs(q + 1);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+  static __device__ __forceinline__ void store(void *p, int64_t i, const float (&v)[8]) {
     float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
     q[0] = make_float4(v[0], v[1], v[2], v[3]);
     q[1] = make_float4(v[4], v[5], v[6], v[7]);
   }
+};
+__device__ __forceinline__ void weights8(const float *p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
+// 1 / (1 + exp(-z)) by the special-function unit: exp2 within 2 ulp, the
+// reciprocal within 1 (an IEEE division takes three times the instructions,
+// and at D = 4096 in bf16 the instructions are as long as the loads).
+__device__ __forceinline__ float sigmoid(float z) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
+}
 __device__ __forceinline__ float act(float z, int kind) {
-  const float s = 1.f / (1.f + __expf(-z));
-  return kind == ONELA_ACT_SILU ? z * s : (kind == ONELA_ACT_SIGMOID ? s : z);
+  return kind == ONELA_ACT_SILU ? z * sigmoid(z) : sigmoid(z);
 }
 
-// Block-wide sum; every thread gets it.  red holds one float per warp.
-__device__ __forceinline__ float block_sum(float x, float *red) {
+// Block-wide sum; every thread gets it.  red holds two sets of one float per
+// warp, used in turn (n counts the sums): the one barrier of a sum keeps the
+// next-but-one from writing over it.
+__device__ __forceinline__ float block_sum(float x, float (&red)[2][32], int &n) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   const int warps = blockDim.x >> 5;
   if (warps == 1) return x;
+  float *r = red[n++ & 1];
+  if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = x;
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-  __syncthreads();
-  float s = (int)(threadIdx.x & 31) < warps ? red[threadIdx.x & 31] : 0.f;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  float s = 0.f;
+  for (int w = 0; w < warps; w += 4) {
+    const float4 q = *reinterpret_cast<const float4 *>(r + w);  // past the last warp: zeros
+    s += (q.x + q.y) + (q.z + q.w);
+  }
   return s;
 }
 
-// One CTA per row, kV vectors of 8 channels per thread (vector e of thread t
-// holds channels 8 (t + e * threads) ..).
-template <int kV>
-__global__ void __launch_bounds__(1024) block_norm_vec(BlockNormParams p) {
-  extern __shared__ float gsum[];  // per vector, its sum of squares (group norms)
-  __shared__ float red[32];
-  const int tid = threadIdx.x, nt = blockDim.x;
-  const int64_t row = blockIdx.x;
-  const int nv = p.D / 8;
-  float v[kV][8], xr[kV][8], gt[kV][8];
+// A CTA takes rows blockIdx.x, + gridDim.x, ..., kV vectors of 8 channels per
+// thread (vector e of thread t holds channels 8 (t + e * threads) ..).  With
+// more rows than CTAs at once the weights stay in shared memory (w_post,
+// alpha and scale as one factor), for they are as many bytes as a row in fp32, and
+// the next row is loaded before this one is reduced, so that loads are always
+// under way.  kLoop = false: a row per CTA, weights from global memory (few rows:
+// latency is what counts, and nothing would be reused).
+template <bool kYBf, bool kBf, int kV, bool kLoop, int kMaxThreads = 512>
+__global__ void __launch_bounds__(kMaxThreads, kV == 4 ? 1 : 2) block_norm_vec(BlockNormParams p) {
+  // kLoop: [D] factor of u, [D] w_pre; then, for group norms that do not fit a warp, [D / 8] sums.
+  extern __shared__ __align__(16) float sm[];
+  __shared__ __align__(16) float red[2][32];
+  int sums = 0;
+  const int tid = threadIdx.x, nt = blockDim.x, nv = p.D / 8, gv = p.group / 8;
+  if (tid < 64) red[tid >> 5][tid & 31] = 0.f;
+  __syncthreads();
+  float *fac = sm, *wpre = sm + p.D, *gsum = kLoop ? sm + 2 * p.D : sm;
+  const bool in_warp = gv <= 32 && (gv & (gv - 1)) == 0;  // a group is an aligned power of two of lanes
+  auto factor = [&](int c, float (&w)[8]) {               // of u at vector c: w_post * alpha * scale
+    if (p.w_post) weights8(p.w_post + (8 * c) % p.group, w);
+    else
 #pragma unroll
-  for (int e = 0; e < kV; ++e) {
-    const int c = tid + e * nt;
-    if (c < nv) {
-      if (p.y) ld8(p.y, row * p.y_stride + 8 * c, p.y_bf16, v[e]);
-      if (p.x) ld8(p.x, row * p.x_stride + 8 * c, p.bf16, xr[e]);
-      if (p.gate) ld8(p.gate, row * p.gate_stride + 8 * c, p.bf16, gt[e]);
+      for (int i = 0; i < 8; ++i) w[i] = 1.f;
+    float z[8];
+    if (p.scale) weights8(p.scale + 8 * c, z);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] *= p.scale ? p.alpha * z[i] : p.alpha;
+  };
+  if (kLoop) {
+    for (int c = tid; c < nv; c += nt) {
+      float w[8];
+      factor(c, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) fac[8 * c + i] = w[i];
+      if (p.w_pre) {
+        weights8(p.w_pre + 8 * c, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) wpre[8 * c + i] = w[i];
+      }
     }
+    __syncthreads();
   }
-  if (p.y) {
-    float sq[kV];
-    float s = 0.f;
+  Vec<kYBf> y[kV];
+  Vec<kBf> x[kV], g[kV];
+  auto fetch = [&](int64_t row) {
 #pragma unroll
     for (int e = 0; e < kV; ++e) {
-      sq[e] = 0.f;
-      if (tid + e * nt < nv) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sq[e] += v[e][i] * v[e][i];
+      const int c = tid + e * nt;
+      if (c < nv) {
+        if (p.y) y[e].load(p.y, row * p.y_stride + 8 * c);
+        if (p.gate) g[e].load(p.gate, row * p.gate_stride + 8 * c);
+        if (p.x) x[e].load(p.x, row * p.x_stride + 8 * c);
       }
-      s += sq[e];
     }
+  };
+  int64_t row = blockIdx.x;
+  fetch(row);
+  for (;;) {
+    float v[kV][8];  // y, then x'
     float inv[kV];
-    if (p.w_post) {
-      if (p.group == p.D) {
-        const float t = rsqrtf(block_sum(s, red) / (float)p.D + p.eps);
+    if (p.y) {
+      float sq[kV], s = 0.f;
 #pragma unroll
-        for (int e = 0; e < kV; ++e) inv[e] = t;
-      } else {
-        const int gv = p.group / 8;
+      for (int e = 0; e < kV; ++e) {
+        sq[e] = 0.f;
+        if (tid + e * nt < nv) {
+          y[e].get(v[e]);
 #pragma unroll
-        for (int e = 0; e < kV; ++e)
-          if (tid + e * nt < nv) gsum[tid + e * nt] = sq[e];
-        __syncthreads();
+          for (int i = 0; i < 8; ++i) sq[e] += v[e][i] * v[e][i];
+        }
+        s += sq[e];
+        inv[e] = 1.f;
+      }
+      if (p.w_post) {
+        if (p.group == p.D) {
+          const float t = rsqrtf(block_sum(s, red, sums) / (float)p.D + p.eps);
 #pragma unroll
-        for (int e = 0; e < kV; ++e) {
-          const int c = tid + e * nt;
-          float t = 0.f;
-          if (c < nv) {
-            const int g0 = c / gv * gv;
-            for (int j = 0; j < gv; ++j) t += gsum[g0 + j];
+          for (int e = 0; e < kV; ++e) inv[e] = t;
+        } else if (in_warp) {
+#pragma unroll
+          for (int e = 0; e < kV; ++e) {
+            float t = sq[e];
+            for (int o = gv >> 1; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+            inv[e] = rsqrtf(t / (float)p.group + p.eps);
           }
-          inv[e] = rsqrtf(t / (float)p.group + p.eps);
+        } else {
+          __syncthreads();  // the last row's sums are read
+#pragma unroll
+          for (int e = 0; e < kV; ++e)
+            if (tid + e * nt < nv) gsum[tid + e * nt] = sq[e];
+          __syncthreads();
+#pragma unroll
+          for (int e = 0; e < kV; ++e) {
+            const int c = tid + e * nt;
+            float t = 0.f;
+            if (c < nv)
+              for (int j = c / gv * gv; j < c / gv * gv + gv; ++j) t += gsum[j];
+            inv[e] = rsqrtf(t / (float)p.group + p.eps);
+          }
         }
       }
     }
-#pragma unroll
-    for (int e = 0; e < kV; ++e) {
-      const int c = tid + e * nt;
-      if (c >= nv) continue;
-      float wp[8], sc[8];
-      if (p.w_post) ld8(p.w_post, 8 * c % p.group, 0, wp);
-      if (p.scale) ld8(p.scale, 8 * c, 0, sc);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float u = v[e][i];
-        if (p.w_post) u = u * inv[e] * wp[i];
-        if (p.gate) u *= act(gt[e][i], p.act);
-        u *= p.alpha;
-        if (p.scale) u *= sc[i];
-        v[e][i] = p.x ? xr[e][i] + u : u;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < kV; ++e)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[e][i] = xr[e][i];
-  }
-  if (p.x_out) {
-#pragma unroll
-    for (int e = 0; e < kV; ++e)
-      if (tid + e * nt < nv) st8(p.x_out, row * p.D + 8 * (tid + e * nt), p.bf16, v[e]);
-  }
-  if (p.w_pre) {
     float s = 0.f;
 #pragma unroll
-    for (int e = 0; e < kV; ++e)
-      if (tid + e * nt < nv) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s += v[e][i] * v[e][i];
-      }
-    const float t = rsqrtf(block_sum(s, red) / (float)p.D + p.eps);
-#pragma unroll
     for (int e = 0; e < kV; ++e) {
       const int c = tid + e * nt;
       if (c >= nv) continue;
-      float w[8];
-      ld8(p.w_pre, 8 * c, 0, w);
+      float z[8];
+      if (p.y) {
+        float w[8];
+        if (kLoop) weights8(fac + 8 * c, w);
+        else factor(c, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] *= v[e][i] * t;
-      st8(p.n_out, row * p.D + 8 * c, p.bf16, w);
+        for (int i = 0; i < 8; ++i) v[e][i] *= inv[e] * w[i];
+        if (p.gate) {
+          g[e].get(z);
+          if (p.act == ONELA_ACT_SILU) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[e][i] *= z[i];
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[e][i] *= sigmoid(z[i]);
+        }
+        if (p.x) {
+          x[e].get(z);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[e][i] += z[i];
+        }
+      } else {
+        x[e].get(v[e]);
+      }
+      if (p.x_out) Vec<kBf>::store(p.x_out, row * p.D + 8 * c, v[e]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[e][i] * v[e][i];
     }
+    const int64_t next = row + gridDim.x;
+    if (kLoop && next < p.N) fetch(next);
+    if (p.w_pre) {
+      const float t = rsqrtf(block_sum(s, red, sums) / (float)p.D + p.eps);
+#pragma unroll
+      for (int e = 0; e < kV; ++e) {
+        const int c = tid + e * nt;
+        if (c >= nv) continue;
+        float w[8];
+        weights8(kLoop ? wpre + 8 * c : p.w_pre + 8 * c, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] *= v[e][i] * t;
+        Vec<kBf>::store(p.n_out, row * p.D + 8 * c, w);
+      }
+    }
+    if (!kLoop || next >= p.N) return;
+    row = next;
   }
 }
 
@@ -184,9 +267,12 @@ __global__ void __launch_bounds__(1024) block_norm_vec(BlockNormParams p) {
 // memory, element by element.
 __global__ void __launch_bounds__(256) block_norm_any(BlockNormParams p) {
   extern __shared__ float buf[];  // [D] the row, then [D / group] the groups' factors
-  __shared__ float red[32];
+  __shared__ __align__(16) float red[2][32];
+  int sums = 0;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row = blockIdx.x;
+  if (tid < 64) red[tid >> 5][tid & 31] = 0.f;
+  __syncthreads();
   float *inv = buf + p.D;
   if (p.y) {
     for (int c = tid; c < p.D; c += 256) buf[c] = ld(p.y, row * p.y_stride + c, p.y_bf16);
@@ -196,7 +282,7 @@ __global__ void __launch_bounds__(256) block_norm_any(BlockNormParams p) {
       if (groups == 1) {
         float s = 0.f;
         for (int c = tid; c < p.D; c += 256) s += buf[c] * buf[c];
-        s = block_sum(s, red);
+        s = block_sum(s, red, sums);
         if (tid == 0) inv[0] = rsqrtf(s / (float)p.D + p.eps);
       } else {
         for (int g = warp; g < groups; g += 8) {
@@ -226,16 +312,50 @@ __global__ void __launch_bounds__(256) block_norm_any(BlockNormParams p) {
     s += t * t;
   }
   if (p.w_pre) {
-    const float t = rsqrtf(block_sum(s, red) / (float)p.D + p.eps);
+    const float t = rsqrtf(block_sum(s, red, sums) / (float)p.D + p.eps);
     for (int c = tid; c < p.D; c += 256) st(p.n_out, row * p.D + c, buf[c] * t * p.w_pre[c], p.bf16);
   }
 }
 
-template <int kV>
+template <bool kYBf, bool kBf, int kV, int kMaxThreads = 512>
 cudaError_t run_vec(const BlockNormParams &p, int threads, cudaStream_t s) {
-  const size_t smem = p.y && p.w_post && p.group != p.D ? (size_t)p.D / 8 * 4 : 0;
-  block_norm_vec<kV><<<(unsigned)p.N, threads, smem, s>>>(p);
+  const int gv = p.group / 8;
+  const bool sums = p.y && p.w_post && p.group != p.D && !(gv <= 32 && (gv & (gv - 1)) == 0);
+  const size_t gs = sums ? (size_t)p.D / 8 * 4 : 0;
+  block_norm_vec<kYBf, kBf, kV, false, kMaxThreads><<<(unsigned)p.N, threads, gs, s>>>(p);
   return cudaGetLastError();
+}
+
+// Rows looping over CTAs; false if there are too few rows for the CTAs that run at once.
+template <bool kYBf, bool kBf, int kV>
+bool run_loop(const BlockNormParams &p, int threads, cudaStream_t s, cudaError_t &e) {
+  const int gv = p.group / 8;
+  const bool sums = p.y && p.w_post && p.group != p.D && !(gv <= 32 && (gv & (gv - 1)) == 0);
+  const size_t smem = (size_t)p.D * 8 + (sums ? (size_t)p.D / 8 * 4 : 0);
+  const int per_sm = std::max(1, std::min(std::min(1024 / threads, 32), (int)(200 * 1024 / (smem + 1024))));
+  const int64_t ctas = (int64_t)kSMs * per_sm;
+  if (p.N < 4 * ctas) return false;
+  auto f = block_norm_vec<kYBf, kBf, kV, true>;
+  e = ensure_smem_limit((const void *)f, smem);
+  if (e == cudaSuccess) {
+    f<<<(unsigned)ctas, threads, smem, s>>>(p);
+    e = cudaGetLastError();
+  }
+  return true;
+}
+
+template <bool kYBf, bool kBf>
+cudaError_t run_types(const BlockNormParams &p, cudaStream_t s) {
+  const int nv = p.D / 8;
+  auto threads = [nv](int per) { return ((nv + per - 1) / per + 31) / 32 * 32; };
+  cudaError_t e;
+  // Looping, two vectors a thread from 256 vectors on: fewer warps to wait for at a sum.
+  if (nv <= 256 ? run_loop<kYBf, kBf, 1>(p, threads(1), s, e) : nv <= 1024 && run_loop<kYBf, kBf, 2>(p, threads(2), s, e))
+    return e;
+  if (nv <= 512) return run_vec<kYBf, kBf, 1>(p, threads(1), s);
+  if (nv <= 1024) return run_vec<kYBf, kBf, 2>(p, threads(2), s);
+  if (nv <= 2048) return run_vec<kYBf, kBf, 4>(p, threads(4), s);
+  return run_vec<kYBf, kBf, 4, 1024>(p, threads(4), s);
 }
 
 }  // namespace
@@ -248,11 +368,8 @@ cudaError_t launch_block_norm(const BlockNormParams &p, cudaStream_t s) {
                            (p.x ? (uint64_t)p.x_stride : 0);
   const bool vec = p.D % 8 == 0 && p.group % 8 == 0 && (ptrs & 15) == 0 && strides % 8 == 0;
   if (vec) {
-    const int nv = p.D / 8;
-    auto threads = [nv](int per) { return ((nv + per - 1) / per + 31) / 32 * 32; };
-    if (nv <= 512) return run_vec<1>(p, threads(1), s);
-    if (nv <= 1024) return run_vec<2>(p, threads(2), s);
-    return run_vec<4>(p, threads(4), s);
+    if (p.y_bf16) return p.bf16 ? run_types<true, true>(p, s) : run_types<true, false>(p, s);
+    return p.bf16 ? run_types<false, true>(p, s) : run_types<false, false>(p, s);
   }
   const size_t smem = (size_t)(p.D + p.D / p.group) * 4;
   cudaError_t e = ensure_smem_limit((const void *)block_norm_any, smem);
