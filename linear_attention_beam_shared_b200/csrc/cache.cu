@@ -85,12 +85,16 @@ constexpr int kSelWarps = kSel / 32;
 constexpr int kBins = 2048;       // 11 bits at a time: 11 + 11 + 10
 constexpr int kSelKeys = 16384;   // keys of its stretch that a CTA keeps in shared memory (64 KB: two CTAs per SM)
 
+constexpr int kCand = 2048;       // positions in the threshold's first bin that a CTA lists
+
 struct EvictSel {
-  uint32_t hist[3][kBins];  // by pass
+  alignas(16) uint32_t hist[3][kBins];  // by digit
   uint32_t warp[kSelWarps];
   uint32_t above[kSelWarps], equal[kSelWarps];  // by warp: keys above the threshold, keys equal to it
-  uint32_t totals[2];       // of the CTA, read by the cluster
-  uint32_t prefix, want;
+  uint32_t totals[2];    // of the CTA, read by the cluster
+  uint32_t found[3][2];  // by digit: the threshold's digits so far, and how many of its bin are wanted
+  uint32_t ncand;
+  int cand[kCand];
 };
 
 // Block-wide exclusive sum of x.
@@ -118,13 +122,21 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t *warp_sums) 
 // One cluster per (request, head): the positions that stay, in order, to kept.
 // The threshold is the want-th largest key of the positions before the recent
 // ones; keys above it stay, and the first keys equal to it until want is met.
-// Every CTA of the cluster takes one stretch of the positions: three passes
-// over its keys build histograms of the digits that still match, the cluster's
-// histograms are added through distributed shared memory, and every CTA finds
-// the same digit.  Then each warp counts and writes a run of positions of its
-// own, so that no barrier sits inside the loops.
+// Every CTA of the cluster takes one stretch of the positions and every warp
+// a run of that.  The threshold is found digit by digit (11, 11 and 10 bits)
+// from histograms of the keys that match so far, the cluster's added up through distributed
+// shared memory, so that every CTA finds the same digit.
+//
+// With 32 rows of 65500 positions on every SM the instructions bound it, so
+// all keys are looked at three times only: when they are loaded (first
+// digit), once to list the keys of the threshold's first bin (few, unless
+// weights are nearly equal: then every key is looked at again) and count those
+// above it, and to write the positions.  Positions past the row have key 0,
+// the lowest (NaN's): they come last among equals, so want never reaches them.
+// kBig: stretches beyond shared memory are read from the weights each time.
+template <bool kBig>
 __global__ void __launch_bounds__(kSel, 2) evict_select(CacheEvictParams p) {
-  extern __shared__ uint32_t keys[];
+  extern __shared__ __align__(16) uint32_t keys[];
   __shared__ EvictSel sm;
   cg::cluster_group cluster = cg::this_cluster();
   const int csize = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -134,7 +146,6 @@ __global__ void __launch_bounds__(kSel, 2) evict_select(CacheEvictParams p) {
   const int given = p.lengths[r];
   const int len = given < 0 ? 0 : (given > cap ? (int)cap : given);
   const int n = min(len, p.keep), rec = min(p.recent, n), free_len = len - rec, want = n - rec;
-  const float *mass = p.mass + (int64_t)rh * cap;
   int32_t *kept = p.kept + (int64_t)rh * p.keep;
   if (h == 0 && rank == 0 && tid == 0) {
     p.dst_lengths[r] = n;
@@ -149,119 +160,193 @@ __global__ void __launch_bounds__(kSel, 2) evict_select(CacheEvictParams p) {
   }
   if (want == 0) return;
 
-  const int seg = ((free_len + csize - 1) / csize + kSel - 1) / kSel * kSel;
+  // Stretches of 32 runs of a multiple of 128: only the row's last one has positions that are not there.
+  const int seg = ((free_len + csize - 1) / csize + 4095) / 4096 * 4096;
   const int s0 = min(free_len, rank * seg), sn = min(free_len, s0 + seg) - s0;
-  const float *mine = mass + s0;
-  const int in_smem = min(sn, kSelKeys);
-  auto key_at = [&](int e) { return e < in_smem ? keys[e] : orderable(mine[e]); };
-  for (int e = tid; e < 3 * kBins; e += kSel) sm.hist[0][e] = 0;
-  if (tid == 0) {
-    sm.prefix = 0;
-    sm.want = (uint32_t)want;
-  }
-  __syncthreads();
-  uint32_t mask = 0;
-  int shift = 21, bits = 11;
-  for (int pass = 0; pass < 3; ++pass) {
-    const uint32_t prefix = sm.prefix, digit = (1u << bits) - 1u;
-    uint32_t *hist = sm.hist[pass];
-    auto count = [&](uint32_t key) {
-      if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & digit], 1u);
-    };
-    int e = tid;
-    for (; e + 7 * kSel < sn; e += 8 * kSel) {
-      uint32_t key[8];
-      if (pass == 0) {
-        float f[8];
+  const int run = ((sn + kSelWarps - 1) / kSelWarps + 127) / 128 * 128;  // positions of a warp
+  const float *mine = p.mass + (int64_t)rh * cap + s0;
+  const bool wide = (reinterpret_cast<uintptr_t>(mine) & 15) == 0;
+  // Keys e .. e + 3 of the stretch, e a multiple of 4.
+  auto fresh4 = [&](int e, uint32_t (&k)[4]) {
+    if (wide && e + 4 <= sn) {
+      const float4 v = *reinterpret_cast<const float4 *>(mine + e);
+      k[0] = orderable(v.x);
+      k[1] = orderable(v.y);
+      k[2] = orderable(v.z);
+      k[3] = orderable(v.w);
+    } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = mine[e + i * kSel];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          key[i] = orderable(f[i]);
-          if (e + i * kSel < in_smem) keys[e + i * kSel] = key[i];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) key[i] = key_at(e + i * kSel);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) count(key[i]);
+      for (int i = 0; i < 4; ++i) k[i] = e + i < sn ? orderable(mine[e + i]) : 0u;
     }
-    for (; e < sn; e += kSel) {
-      const uint32_t key = pass == 0 ? orderable(mine[e]) : key_at(e);
-      if (pass == 0 && e < in_smem) keys[e] = key;
-      count(key);
+  };
+  auto keys4 = [&](int e, uint32_t (&k)[4]) {
+    if constexpr (kBig) {
+      fresh4(e, k);
+    } else {
+      const uint4 v = *reinterpret_cast<const uint4 *>(keys + e);
+      k[0] = v.x;
+      k[1] = v.y;
+      k[2] = v.z;
+      k[3] = v.w;
     }
+  };
+  auto sync = [&] {
     if (csize > 1) cluster.sync();
     else __syncthreads();
-    // From the top bin down: thread t takes bins nb - 1 - 2t and nb - 2 - 2t of all CTAs.
-    const int b0 = (1 << bits) - 1 - 2 * tid;
+  };
+  uint32_t prefix = 0, left = (uint32_t)want;
+  // The digit of the threshold at `shift`, from the cluster's histograms: from
+  // the top bin down, thread t takes bins nb - 1 - 2t and nb - 2 - 2t.
+  auto find = [&](int pass, int shift, int nb) {
+    const int b1 = nb - 2 - 2 * tid;
     uint32_t c0 = 0, c1 = 0;
-    if (b0 >= 1)
+    if (b1 >= 0) {
+#pragma unroll 4
       for (int c = 0; c < csize; ++c) {
-        const uint32_t *other = csize > 1 ? cluster.map_shared_rank(hist, c) : hist;
-        c0 += other[b0];
-        c1 += other[b0 - 1];
+        const uint2 v = *reinterpret_cast<const uint2 *>(
+            csize > 1 ? cluster.map_shared_rank(&sm.hist[pass][b1], c) : &sm.hist[pass][b1]);
+        c0 += v.y;
+        c1 += v.x;
       }
+    }
     const uint32_t above = block_scan(c0 + c1, sm.warp);
-    const uint32_t w = sm.want;
-    __syncthreads();
-    if (above < w && w <= above + c0 + c1) {  // exactly one thread
-      const bool second = w > above + c0;
-      sm.prefix = prefix | ((uint32_t)(second ? b0 - 1 : b0) << shift);
-      sm.want = w - above - (second ? c0 : 0);
+    if (above < left && left <= above + c0 + c1) {  // exactly one thread
+      const bool second = left > above + c0;
+      sm.found[pass][0] = prefix | ((uint32_t)(second ? b1 : b1 + 1) << shift);
+      sm.found[pass][1] = left - above - (second ? c0 : 0);
     }
     __syncthreads();
-    mask |= digit << shift;
-    bits = pass == 0 ? 11 : 10;
-    shift -= bits;
-  }
-  const uint32_t thr = sm.prefix, ties = sm.want;
-  // Each warp has a run of positions; its keys above and equal, then those of
-  // the warps and CTAs before it.
-  const int run = ((sn + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
-  const int w0 = min(sn, warp * run), w1 = min(sn, w0 + run);
-  uint32_t g = 0, q = 0;
-  for (int e = w0 + lane; e < w1; e += 32) {
-    const uint32_t key = key_at(e);
-    g += key > thr;
-    q += key == thr;
-  }
+    prefix = sm.found[pass][0];
+    left = sm.found[pass][1];
+  };
+  for (int e = tid; e < 3 * kBins / 4; e += kSel) reinterpret_cast<uint4 *>(sm.hist)[e] = make_uint4(0, 0, 0, 0);
+  if (tid == 0) sm.ncand = 0;
+  __syncthreads();
+  const int w0 = warp * run + 4 * lane, w1 = (warp + 1) * run;  // this lane's keys: w0, w0 + 128, ... four each
+#pragma unroll 4
+  for (int e = w0; e < w1; e += 128) {
+    uint32_t k[4];
+    fresh4(e, k);
+    if (!kBig) *reinterpret_cast<uint4 *>(keys + e) = make_uint4(k[0], k[1], k[2], k[3]);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    g += __shfl_xor_sync(0xffffffffu, g, o);
-    q += __shfl_xor_sync(0xffffffffu, q, o);
+    for (int i = 0; i < 4; ++i) atomicAdd(&sm.hist[0][k[i] >> 21], 1u);
   }
+  sync();
+  find(0, 21, 2048);
+  uint32_t g = 0, q = 0;
+#pragma unroll 1
+  for (int e = w0; e < w1; e += 128) {
+    uint32_t k[4];
+    keys4(e, k);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t d = k[i] >> 21;
+      g += d > prefix >> 21;
+      if (d == prefix >> 21) {
+        atomicAdd(&sm.hist[1][(k[i] >> 10) & 2047u], 1u);
+        const uint32_t at = atomicAdd(&sm.ncand, 1u);
+        if (at < kCand) sm.cand[at] = e + i;
+      }
+    }
+  }
+  sync();
+  const uint32_t ncand = sm.ncand;
+  const bool listed = ncand <= kCand;
+  auto key_of = [&](int e) { return kBig ? orderable(mine[e]) : keys[e]; };  // of a listed position
+  find(1, 10, 2048);
+  if (listed) {
+    for (uint32_t c = tid; c < ncand; c += kSel) {
+      const int e = sm.cand[c];
+      const uint32_t key = e < sn ? key_of(e) : 0u;
+      if (((key ^ prefix) >> 10) == 0) atomicAdd(&sm.hist[2][key & 1023u], 1u);
+    }
+  } else {
+#pragma unroll 1
+    for (int e = w0; e < w1; e += 128) {
+      uint32_t k[4];
+      keys4(e, k);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (((k[i] ^ prefix) >> 10) == 0) atomicAdd(&sm.hist[2][k[i] & 1023u], 1u);
+    }
+  }
+  sync();
+  find(2, 0, 1024);
+  const uint32_t thr = prefix, ties = left;
+  // Keys above and equal, by warp; then those of the warps and CTAs before.
+  if (!listed) {
+    g = 0;
+#pragma unroll 1
+    for (int e = w0; e < w1; e += 128) {
+      uint32_t k[4];
+      keys4(e, k);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        g += k[i] > thr;
+        q += k[i] == thr;
+      }
+    }
+  }
+  g = __reduce_add_sync(0xffffffffu, g);
+  q = __reduce_add_sync(0xffffffffu, q);
   if (lane == 0) {
     sm.above[warp] = g;
     sm.equal[warp] = q;
   }
   __syncthreads();
+  if (listed) {
+    for (uint32_t c = tid; c < ncand; c += kSel) {
+      const int e = sm.cand[c];
+      const uint32_t key = e < sn ? key_of(e) : 0u;
+      if (key > thr) atomicAdd(&sm.above[e / run], 1u);
+      if (key == thr) atomicAdd(&sm.equal[e / run], 1u);
+    }
+    __syncthreads();
+  }
   uint32_t gb = sm.above[lane], qb = sm.equal[lane];
-  const uint32_t g_all = __reduce_add_sync(0xffffffffu, gb), q_all = __reduce_add_sync(0xffffffffu, qb);
-  gb = __reduce_add_sync(0xffffffffu, lane < warp ? gb : 0);
-  qb = __reduce_add_sync(0xffffffffu, lane < warp ? qb : 0);
   if (csize > 1) {
+    const uint32_t g_all = __reduce_add_sync(0xffffffffu, gb), q_all = __reduce_add_sync(0xffffffffu, qb);
     if (tid == 0) {
       sm.totals[0] = g_all;
       sm.totals[1] = q_all;
     }
-    cluster.sync();
-    for (int c = 0; c < rank; ++c) {
-      const uint32_t *other = cluster.map_shared_rank(sm.totals, c);
-      gb += other[0];
-      qb += other[1];
-    }
   }
-  for (int e0 = w0; e0 < w1; e0 += 32) {
-    const int e = e0 + lane;
-    const uint32_t key = e < w1 ? key_at(e) : 0u;
-    const bool is_g = e < w1 && key > thr, is_q = e < w1 && key == thr;
-    const uint32_t mg = __ballot_sync(0xffffffffu, is_g), mq = __ballot_sync(0xffffffffu, is_q), below = (1u << lane) - 1u;
-    const uint32_t gi = gb + __popc(mg & below), qi = qb + __popc(mq & below);
-    if (is_g || (is_q && qi < ties)) kept[gi + min(qi, ties)] = s0 + e;
-    gb += __popc(mg);
-    qb += __popc(mq);
+  gb = __reduce_add_sync(0xffffffffu, lane < warp ? gb : 0);
+  qb = __reduce_add_sync(0xffffffffu, lane < warp ? qb : 0);
+  if (csize > 1) {
+    cluster.sync();
+    const uint32_t *other = cluster.map_shared_rank(sm.totals, lane < rank ? lane : rank);
+    gb += __reduce_add_sync(0xffffffffu, lane < rank ? other[0] : 0);
+    qb += __reduce_add_sync(0xffffffffu, lane < rank ? other[1] : 0);
+  }
+#pragma unroll 1
+  for (int e = w0; e < w1; e += 128) {
+    uint32_t k[4], mine2 = 0;  // above in the low half, equal in the high half
+    keys4(e, k);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mine2 += (k[i] > thr ? 1u : 0u) + (k[i] == thr ? 0x10000u : 0u);
+    if (__any_sync(0xffffffffu, mine2)) {
+      uint32_t incl = mine2;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      const uint32_t before = incl - mine2, all2 = __shfl_sync(0xffffffffu, incl, 31);
+      if (mine2) {
+        uint32_t gi = gb + (before & 0xffffu), qi = qb + (before >> 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (k[i] > thr) kept[gi++ + min(qi, ties)] = s0 + e + i;
+          else if (k[i] == thr) {
+            if (qi < ties) kept[gi + qi] = s0 + e + i;
+            ++qi;
+          }
+        }
+      }
+      gb += all2 & 0xffffu;
+      qb += all2 >> 16;
+    }
   }
   if (csize > 1) cluster.sync();  // the others have read this CTA's totals
 }
@@ -397,15 +482,16 @@ cudaError_t launch_cache_evict(const CacheEvictParams &p, cudaStream_t s) {
   const int64_t cap = (int64_t)p.page * p.row_pages;
   int csize = 1;
   while (csize < 8 && (int64_t)csize * kSelKeys < cap) csize *= 2;
-  const int64_t per = std::min<int64_t>(kSelKeys, (cap + csize - 1) / csize + kSel);
+  const int64_t stretch = ((cap + csize - 1) / csize + 4095) / 4096 * 4096;
+  const bool big = stretch > kSelKeys;
   const int64_t sel_grid = (int64_t)p.R * p.Hkv * csize;
   if (sel_grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  cudaError_t e = ensure_smem_limit((const void *)evict_select, kSelKeys * 4);
+  cudaError_t e = ensure_smem_limit((const void *)evict_select<false>, kSelKeys * 4);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)sel_grid);
   cfg.blockDim = dim3(kSel);
-  cfg.dynamicSmemBytes = (size_t)per * 4;
+  cfg.dynamicSmemBytes = big ? 0 : (size_t)stretch * 4;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -413,7 +499,7 @@ cudaError_t launch_cache_evict(const CacheEvictParams &p, cudaStream_t s) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, evict_select, p);
+  e = cudaLaunchKernelEx(&cfg, big ? evict_select<true> : evict_select<false>, p);
   if (e != cudaSuccess) return e;
   const uint64_t all = addr(p.dst_k) | addr(p.dst_v) | addr(p.k_pool) | addr(p.v_pool) | (uint64_t)p.row_bytes;
   const int u = unit_of(all), per_row = p.row_bytes / u;

@@ -362,6 +362,25 @@ def test_evict_all_weights_equal_and_long_rows():
     run_evict(cache, rng.random(shape).astype(np.float32), 39999, 0, 1, 64, 8, "bf16")
 
 
+@pytest.mark.parametrize("kind", ["smooth", "nan", "few_numbers", "levels"])
+@pytest.mark.parametrize("n,keep", [(16384, 9000), (16385, 16000), (40000, 25000), (131072, 100000), (131073, 60000),
+                                    (150000, 149000)])
+def test_evict_rows_of_several_ctas(n, keep, kind):
+    """Rows up to and past what a cluster keeps in shared memory, with ties
+    that run across its CTAs' borders."""
+    rng = np.random.default_rng(n)
+    cache = Cache(rng, [n, n // 3], 1, 64, 4, "f32")
+    shape = (2, 1, cache.row_pages * 64)
+    m = np.exp(2 * rng.standard_normal(shape)).astype(np.float32)
+    if kind == "nan":
+        m[:] = np.nan
+    if kind == "few_numbers":
+        m = np.where(rng.random(shape) < 0.9, np.float32(np.nan), m)
+    if kind == "levels":
+        m = (1 + rng.integers(0, 3, shape) * 2.0 ** -20).astype(np.float32)
+    run_evict(cache, m, keep, 7, 1, 64, 4, "f32")
+
+
 def test_evict_bad_pages_and_lengths():
     import linear_attention_beam_shared_b200 as L
     rng = np.random.default_rng(4)
