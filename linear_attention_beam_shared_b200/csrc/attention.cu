@@ -27,174 +27,6 @@ constexpr int kThreads = 128;
 constexpr int kRows = 8;   // query rows per CTA
 constexpr int kToks = 32;  // tokens per step
 
-// The general kernel: any d, fp32 or bf16.  A CTA takes one part of the
-// prompts, one key-value head and 8 query rows; per step of 32 tokens K and V rows go
-// through shared memory as fp32, each warp forms two rows' scores (lane =
-// token), and each thread keeps one or two columns of the 8 outputs.
-template <typename T, bool kVec>
-__global__ void __launch_bounds__(kThreads) attn_simt(AttnParams p) {
-  extern __shared__ __align__(16) float smem[];
-  __shared__ PlanSmem plan;
-  __shared__ float ps[kToks][kRows];
-  __shared__ float corr[kRows];
-  __shared__ int ok[kToks];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int dp = (p.d + 3) & ~3, dk = dp + 4;
-  float *qs = smem, *ks = qs + kRows * dp, *vs = ks + kToks * dk;
-
-  const int rt = blockIdx.x % p.row_tiles, uh = blockIdx.x / p.row_tiles;
-  const int h = uh % p.Hkv;
-  ptx::pdl_launch_dependents();
-  PlanWalk walk;
-  walk.begin<kThreads>(p, plan, uh / p.Hkv);
-  const T *q = static_cast<const T *>(p.q), *k = static_cast<const T *>(p.k), *v = static_cast<const T *>(p.v);
-  const int m0 = rt * kRows;
-  while (walk.next(p)) {
-  const int r = walk.r, lo = walk.lo, hi = walk.hi;
-  __syncthreads();  // the previous piece's shared memory is read
-  if (p.direct && h == 0 && rt == 0 && tid == 0 && p.lengths[r] != hi) set_status(p.status, kStatusLength);
-  for (int i = warp; i < kRows; i += 4) {
-    const int m = m0 + i;
-    const int w = m / p.G, hq = h * p.G + m % p.G;
-    for (int c = lane; c < dp; c += 32)
-      qs[i * dp + c] = (m < p.M && c < p.d) ? to_f(q[((int64_t)r * p.W + w) * p.q_stride + (int64_t)hq * p.d + c]) : 0.f;
-  }
-  // Columns past d of the key rows stay zero.
-  for (int i = tid; i < kToks; i += kThreads)
-    for (int c = p.d; c < dp; ++c) ks[i * dk + c] = 0.f;
-
-  float acc0[kRows], acc1[kRows], mx[2], sum[2];
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) acc0[i] = acc1[i] = 0.f;
-  mx[0] = mx[1] = -CUDART_INF_F;
-  sum[0] = sum[1] = 0.f;
-  const int c0 = tid, c1 = tid + kThreads;
-
-  for (int t0 = lo; t0 < hi; t0 += kToks) {
-    __syncthreads();  // the previous step's K, V and ps are read
-    for (int i = warp; i < kToks; i += 4) {
-      const int pos = t0 + i;
-      int64_t row = -1;
-      if (pos < hi) {
-        const int pg = p.table[(int64_t)r * p.row_pages + pos / p.page];
-        if (pg >= 0 && pg < p.pages) {
-          row = (((int64_t)pg * p.Hkv + h) * p.page + pos % p.page) * p.d;
-        } else if (lane == 0) {
-          set_status(p.status, kStatusPage);
-        }
-      }
-      if (lane == 0) ok[i] = row >= 0;
-      if constexpr (kVec) {
-        constexpr int kE = 16 / sizeof(T);
-        for (int c = lane * kE; c < p.d; c += 32 * kE) {
-          union { uint4 u; T e[kE]; } a, b;
-          a.u = b.u = make_uint4(0, 0, 0, 0);
-          if (row >= 0) {
-            a.u = *reinterpret_cast<const uint4 *>(k + row + c);
-            b.u = *reinterpret_cast<const uint4 *>(v + row + c);
-          }
-#pragma unroll
-          for (int e = 0; e < kE; e += 4) {
-            *reinterpret_cast<float4 *>(&ks[i * dk + c + e]) =
-                make_float4(to_f(a.e[e]), to_f(a.e[e + 1]), to_f(a.e[e + 2]), to_f(a.e[e + 3]));
-            *reinterpret_cast<float4 *>(&vs[i * dp + c + e]) =
-                make_float4(to_f(b.e[e]), to_f(b.e[e + 1]), to_f(b.e[e + 2]), to_f(b.e[e + 3]));
-          }
-        }
-      } else {
-        for (int c = lane; c < p.d; c += 32) {
-          ks[i * dk + c] = row >= 0 ? to_f(k[row + c]) : 0.f;
-          vs[i * dp + c] = row >= 0 ? to_f(v[row + c]) : 0.f;
-        }
-      }
-    }
-    __syncthreads();
-    float s[2] = {0.f, 0.f};
-    {
-      const float *kr = ks + lane * dk, *qa = qs + (2 * warp) * dp, *qb = qa + dp;
-      for (int c = 0; c < dp; c += 4) {
-        const float4 x = *reinterpret_cast<const float4 *>(kr + c);
-        const float4 a = *reinterpret_cast<const float4 *>(qa + c), b = *reinterpret_cast<const float4 *>(qb + c);
-        s[0] += x.x * a.x + x.y * a.y + x.z * a.z + x.w * a.w;
-        s[1] += x.x * b.x + x.y * b.y + x.z * b.z + x.w * b.w;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int m = m0 + 2 * warp + i;
-      const float x = ok[lane] ? s[i] * p.scale_log2 : -CUDART_INF_F;
-      if (p.scores && m < p.M && t0 + lane < hi)
-        p.scores[(((int64_t)r * p.Hkv + h) * p.M + m) * p.cap + t0 + lane] = x;
-      const float mnew = fmaxf(mx[i], warp_max(x));
-      const float e = exp2_sub(x, mnew), f = exp2_sub(mx[i], mnew);
-      sum[i] = sum[i] * f + warp_sum(e);
-      mx[i] = mnew;
-      ps[lane][2 * warp + i] = e;
-      if (lane == 0) corr[2 * warp + i] = f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      acc0[i] *= corr[i];
-      acc1[i] *= corr[i];
-    }
-    const int n = min(kToks, hi - t0);
-    if (c0 < p.d) {
-      for (int t = 0; t < n; ++t) {
-        const float4 a = *reinterpret_cast<const float4 *>(&ps[t][0]), b = *reinterpret_cast<const float4 *>(&ps[t][4]);
-        const float e[kRows] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        const float x0 = vs[t * dp + c0];
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) acc0[i] += e[i] * x0;
-        if (c1 < p.d) {
-          const float x1 = vs[t * dp + c1];
-#pragma unroll
-          for (int i = 0; i < kRows; ++i) acc1[i] += e[i] * x1;
-        }
-      }
-    }
-  }
-  __syncthreads();
-  if (p.direct) {
-    // Sums by row through shared memory (each warp holds two rows').
-    if (lane == 0) {
-      corr[2 * warp] = sum[0];
-      corr[2 * warp + 1] = sum[1];
-      ps[0][2 * warp] = mx[0];
-      ps[0][2 * warp + 1] = mx[1];
-    }
-    __syncthreads();
-    T *o = static_cast<T *>(p.o);
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int m = m0 + i;
-      if (m >= p.M) continue;
-      const int64_t row = ((int64_t)r * p.W + m / p.G) * p.Hq + h * p.G + m % p.G;
-      const float inv = corr[i] == 0.f ? 0.f : 1.f / corr[i];
-      if (c0 < p.d) store_f(o + row * p.d + c0, acc0[i] * inv);
-      if (c1 < p.d) store_f(o + row * p.d + c1, acc1[i] * inv);
-      if (tid == 0 && p.lse) p.lse[row] = corr[i] == 0.f ? -CUDART_INF_F : (ps[0][i] + log2f(corr[i])) * kLn2;
-    }
-    continue;
-  }
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int m = m0 + i;
-    if (m >= p.M) continue;
-    float *po = p.part_o + part_row(p, walk.slot, h, m) * p.d;
-    if (c0 < p.d) po[c0] = acc0[i];
-    if (c1 < p.d) po[c1] = acc1[i];
-  }
-  if (lane == 0) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int m = m0 + 2 * warp + i;
-      if (m < p.M) p.part_ml[part_row(p, walk.slot, h, m)] = make_float2(mx[i], sum[i]);
-    }
-  }
-  }
-}
-
 // N consecutive elements as floats.
 template <int N, bool kVec>
 __device__ __forceinline__ void ldn(const float *p, float (&v)[N]) {
@@ -227,6 +59,235 @@ __device__ __forceinline__ void ldn(const __nv_bfloat16 *p, float (&v)[N]) {
   for (int i = 0; i < N / 2; ++i) {
     v[2 * i] = __uint_as_float(u[i] << 16);
     v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+
+// 4-byte asynchronous copy global -> shared; src_bytes = 0 writes zeros without reading src.
+__device__ __forceinline__ void cp_async4_zfill(void *dst, const void *src, uint32_t src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(ptx::smem_u32(dst)), "l"(src), "r"(src_bytes)
+               : "memory");
+}
+
+// Shared memory of the general kernel: q as fp32, then stages of raw K and V
+// rows.  K rows are an odd number of 16-byte chunks apart, so that 32 lanes
+// reading the same chunk of 32 rows meet no bank twice.
+struct SimtLayout {
+  int dp, k_stride, v_stride, stage, stages;  // floats of a q row; bytes of a K row, a V row, a stage
+  __host__ __device__ SimtLayout(int d, int es) {
+    const int row = (d * es + 15) & ~15;
+    dp = row / es;
+    k_stride = row / 16 % 2 ? row : row + 16;
+    v_stride = row;
+    stage = kToks * (k_stride + v_stride);
+    stages = row <= 256 ? 3 : 2;
+  }
+  __host__ __device__ int bytes() const { return kRows * dp * 4 + stages * stage; }
+  // CTAs that fit an SM by shared memory, at most 4 (by registers).
+  int per_sm() const { return std::min(4, std::max(1, 225 * 1024 / (bytes() + 3 * 1024))); }
+};
+
+// The general kernel: any d, fp32 or bf16.  A CTA takes one part of the
+// prompts, one key-value head and 8 query rows.  Steps of 32 tokens pass
+// through a ring of stages filled by asynchronous copies of kUnit bytes: 16,
+// or 4 where rows are no multiple of 16 bytes or not on such boundaries; bf16 rows of odd d
+// by plain loads (kUnit = 2).
+// Per step each warp forms two rows' scores (lane = token: a K chunk from
+// shared memory serves two rows, 8 FMAs for 3 loads), takes their softmax by
+// shuffles, and each thread adds to one or two columns of the 8 outputs (one
+// V element for 8 rows).  In fp32 at d = 128 that is about 100 instructions a
+// token on an SM that can issue 180 in the time the token's rows take to
+// arrive.
+template <typename T, int kUnit>
+__global__ void __launch_bounds__(kThreads, 4) attn_simt(AttnParams p) {
+  extern __shared__ __align__(16) float smem[];
+  __shared__ PlanSmem plan;
+  __shared__ __align__(16) float ps[kToks][kRows];
+  __shared__ __align__(16) float corr[kRows];
+  __shared__ __align__(4) uint8_t there[4][4];  // by stage and warp: which of its 8 tokens are there
+  const SimtLayout L(p.d, sizeof(T));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  float *qs = smem;
+  uint8_t *ring = reinterpret_cast<uint8_t *>(smem + kRows * L.dp);
+
+  const int rt = blockIdx.x % p.row_tiles, uh = blockIdx.x / p.row_tiles;
+  const int h = uh % p.Hkv;
+  ptx::pdl_launch_dependents();
+  PlanWalk walk;
+  walk.begin<kThreads>(p, plan, uh / p.Hkv);
+
+  const T *q = static_cast<const T *>(p.q), *k = static_cast<const T *>(p.k), *v = static_cast<const T *>(p.v);
+  const int m0 = rt * kRows;
+  const int c0 = tid, c1 = tid + kThreads;
+  while (walk.next(p)) {
+    const int r = walk.r, lo = walk.lo, hi = walk.hi, n = (hi - lo + kToks - 1) / kToks;
+    __syncthreads();  // the previous piece's shared memory is read
+    if (p.direct && h == 0 && rt == 0 && tid == 0 && p.lengths[r] != hi) set_status(p.status, kStatusLength);
+    // Element offset of this lane's token of step i (lanes 0 .. 7: the warp's 8 tokens); -1 if it is not there.
+    auto find = [&](int i) -> int64_t {
+      const int pos = lo + i * kToks + warp * 8 + lane;
+      if (lane >= 8 || pos >= hi) return -1;
+      const int pg = p.table[(int64_t)r * p.row_pages + pos / p.page];
+      if (pg < 0 || pg >= p.pages) {
+        set_status(p.status, kStatusPage);
+        return -1;
+      }
+      return (((int64_t)pg * p.Hkv + h) * p.page + pos % p.page) * p.d;
+    };
+    auto fill = [&](int i, int64_t row) {
+      if (i < n) {
+        const int st = i % L.stages;
+        uint8_t *kd = ring + st * L.stage, *vd = kd + kToks * L.k_stride;
+        const uint32_t bits = __ballot_sync(0xffffffffu, row >= 0);
+        if (lane == 0) there[st][warp] = (uint8_t)bits;
+#pragma unroll 4
+        for (int t = 0; t < 8; ++t) {
+          const int64_t at = __shfl_sync(0xffffffffu, row, t);
+          uint8_t *kr = kd + (warp * 8 + t) * L.k_stride, *vr = vd + (warp * 8 + t) * L.v_stride;
+          if constexpr (kUnit == 16) {
+            for (int c = lane * 16; c < p.d * (int)sizeof(T); c += 512) {
+              ptx::cp_async16(kr + c, reinterpret_cast<const uint8_t *>(k + (at < 0 ? 0 : at)) + c, at < 0 ? 0 : 16);
+              ptx::cp_async16(vr + c, reinterpret_cast<const uint8_t *>(v + (at < 0 ? 0 : at)) + c, at < 0 ? 0 : 16);
+            }
+          } else if constexpr (kUnit == 4) {
+            for (int c = lane * 4; c < L.dp * (int)sizeof(T); c += 128) {
+              const bool in = at >= 0 && c < p.d * (int)sizeof(T);
+              const int64_t from = in ? at * (int)sizeof(T) + c : 0;
+              cp_async4_zfill(kr + c, reinterpret_cast<const uint8_t *>(k) + from, in ? 4 : 0);
+              cp_async4_zfill(vr + c, reinterpret_cast<const uint8_t *>(v) + from, in ? 4 : 0);
+            }
+          } else {
+            for (int c = lane; c < L.dp; c += 32) {
+              const bool in = at >= 0 && c < p.d;
+              reinterpret_cast<T *>(kr)[c] = in ? k[at + c] : T(0.f);
+              reinterpret_cast<T *>(vr)[c] = in ? v[at + c] : T(0.f);
+            }
+          }
+        }
+      }
+      ptx::cp_async_commit();
+    };
+    int64_t row = find(0);
+    for (int i = 0; i < L.stages - 1; ++i) {
+      fill(i, row);
+      row = find(i + 1);
+    }
+    for (int i = warp; i < kRows; i += 4) {
+      const int m = m0 + i;
+      const int w = m / p.G, hq = h * p.G + m % p.G;
+      for (int c = lane; c < L.dp; c += 32)
+        qs[i * L.dp + c] =
+            (m < p.M && c < p.d) ? to_f(q[((int64_t)r * p.W + w) * p.q_stride + (int64_t)hq * p.d + c]) : 0.f;
+    }
+
+    float acc0[kRows], acc1[kRows], mx[2], sum[2];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) acc0[i] = acc1[i] = 0.f;
+    mx[0] = mx[1] = -CUDART_INF_F;
+    sum[0] = sum[1] = 0.f;
+
+    for (int i = 0; i < n; ++i) {
+      if (L.stages == 3) ptx::cp_async_wait_group1();
+      else ptx::cp_async_wait_all();
+      __syncthreads();  // step i is there for every warp, step i - 1 read by all
+      fill(i + L.stages - 1, row);
+      row = find(i + L.stages);
+      const int st = i % L.stages;
+      const uint8_t *ks = ring + st * L.stage, *vs = ks + kToks * L.k_stride;
+      const uint32_t live = *reinterpret_cast<const uint32_t *>(there[st]);
+      float s[2] = {0.f, 0.f};
+      {
+        const uint8_t *kr = ks + lane * L.k_stride;
+        const float *qa = qs + (2 * warp) * L.dp, *qb = qa + L.dp;
+        constexpr int kE = 16 / sizeof(T);
+#pragma unroll 4
+        for (int c = 0; c < L.dp; c += kE) {
+          float x[kE];
+          ldn<kE, true>(reinterpret_cast<const T *>(kr) + c, x);
+#pragma unroll
+          for (int e = 0; e < kE; e += 4) {
+            const float4 a = *reinterpret_cast<const float4 *>(qa + c + e), b = *reinterpret_cast<const float4 *>(qb + c + e);
+            s[0] += x[e] * a.x + x[e + 1] * a.y + x[e + 2] * a.z + x[e + 3] * a.w;
+            s[1] += x[e] * b.x + x[e + 1] * b.y + x[e + 2] * b.z + x[e + 3] * b.w;
+          }
+        }
+      }
+      const int pos = lo + i * kToks + lane;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int m = m0 + 2 * warp + e;
+        const float x = (live >> lane) & 1 ? s[e] * p.scale_log2 : -CUDART_INF_F;
+        if (p.scores && m < p.M && pos < hi) p.scores[(((int64_t)r * p.Hkv + h) * p.M + m) * p.cap + pos] = x;
+        const float mnew = fmaxf(mx[e], warp_max(x));
+        const float w = exp2_sub(x, mnew), f = exp2_sub(mx[e], mnew);
+        sum[e] = sum[e] * f + warp_sum(w);
+        mx[e] = mnew;
+        ps[lane][2 * warp + e] = w;
+        if (lane == 0) corr[2 * warp + e] = f;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < kRows; ++e) {
+        acc0[e] *= corr[e];
+        acc1[e] *= corr[e];
+      }
+      const int nt = min(kToks, hi - lo - i * kToks);
+      if (c0 < p.d) {
+        const T *vc = reinterpret_cast<const T *>(vs) + c0;
+        const int step = L.v_stride / (int)sizeof(T);
+#pragma unroll 4
+        for (int t = 0; t < nt; ++t) {
+          const float4 a = *reinterpret_cast<const float4 *>(&ps[t][0]), b = *reinterpret_cast<const float4 *>(&ps[t][4]);
+          const float w[kRows] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+          const float x0 = to_f(vc[t * step]);
+#pragma unroll
+          for (int e = 0; e < kRows; ++e) acc0[e] += w[e] * x0;
+          if (c1 < p.d) {
+            const float x1 = to_f(vc[t * step + kThreads]);
+#pragma unroll
+            for (int e = 0; e < kRows; ++e) acc1[e] += w[e] * x1;
+          }
+        }
+      }
+    }
+    ptx::cp_async_wait_all();
+    __syncthreads();
+    if (p.direct) {
+      // Sums by row through shared memory (each warp holds two rows').
+      if (lane == 0) {
+        corr[2 * warp] = sum[0];
+        corr[2 * warp + 1] = sum[1];
+        ps[0][2 * warp] = mx[0];
+        ps[0][2 * warp + 1] = mx[1];
+      }
+      __syncthreads();
+      T *o = static_cast<T *>(p.o);
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int m = m0 + i;
+        if (m >= p.M) continue;
+        const int64_t orow = ((int64_t)r * p.W + m / p.G) * p.Hq + h * p.G + m % p.G;
+        const float inv = corr[i] == 0.f ? 0.f : 1.f / corr[i];
+        if (c0 < p.d) store_f(o + orow * p.d + c0, acc0[i] * inv);
+        if (c1 < p.d) store_f(o + orow * p.d + c1, acc1[i] * inv);
+        if (tid == 0 && p.lse) p.lse[orow] = corr[i] == 0.f ? -CUDART_INF_F : (ps[0][i] + log2f(corr[i])) * kLn2;
+      }
+      continue;
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int m = m0 + i;
+      if (m >= p.M) continue;
+      float *po = p.part_o + part_row(p, walk.slot, h, m) * p.d;
+      if (c0 < p.d) po[c0] = acc0[i];
+      if (c1 < p.d) po[c1] = acc1[i];
+    }
+    if (lane == 0) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int m = m0 + 2 * warp + i;
+        if (m < p.M) p.part_ml[part_row(p, walk.slot, h, m)] = make_float2(mx[i], sum[i]);
+      }
+    }
   }
 }
 
@@ -449,7 +510,7 @@ size_t plan_call(const onela_attention_config &c, bool want_mass, AttnParams &p,
   p.q_stride = c.q_stride;
   p.scale_log2 = c.scale * kLog2e;
   const AttnKind kind = choose(c, p);
-  int ctas = 4 * kAttnSMs;  // that run at once
+  int ctas = SimtLayout(c.d, c.dtype == ONELA_BF16 ? 2 : 4).per_sm() * kAttnSMs;  // that run at once
   p.rows = kRows;
   p.tile = kToks;
   p.per_slot = 1;
@@ -501,10 +562,10 @@ size_t plan_call(const onela_attention_config &c, bool want_mass, AttnParams &p,
 }
 
 template <typename T>
-cudaError_t run_simt(const AttnParams &p, bool vec, cudaStream_t s) {
-  const int dp = (p.d + 3) & ~3;
-  const size_t smem = (size_t)(kRows * dp + kToks * (dp + 4) + kToks * dp) * 4;
-  auto f = vec ? attn_simt<T, true> : attn_simt<T, false>;
+cudaError_t run_simt(const AttnParams &p, cudaStream_t s) {
+  const size_t smem = (size_t)SimtLayout(p.d, sizeof(T)).bytes();
+  const uint64_t at = (uint64_t)p.d * sizeof(T) | reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v);
+  auto f = at % 16 == 0 ? attn_simt<T, 16> : at % 4 == 0 ? attn_simt<T, 4> : attn_simt<T, 2>;
   const cudaError_t e = ensure_smem_limit((const void *)f, smem);
   if (e != cudaSuccess) return e;
   return launch_kernel(f, (unsigned)((long long)p.parts * p.Hkv * p.row_tiles), kThreads, smem, false, s, p);
@@ -532,14 +593,14 @@ cudaError_t run_join(const AttnParams &p, cudaStream_t s) {
 }
 
 template <typename T>
-cudaError_t run(const AttnParams &p, AttnKind kind, bool vec, cudaStream_t s) {
+cudaError_t run(const AttnParams &p, AttnKind kind, cudaStream_t s) {
   cudaError_t e;
   if (kind == kAttnNarrow) {
     e = launch_attn_narrow(p, s);
   } else if (kind == kAttnWide) {
     e = launch_attn_wide(p, s);
   } else {
-    e = run_simt<T>(p, vec, s);
+    e = run_simt<T>(p, s);
   }
   if (e != cudaSuccess || p.direct) return e;
 
@@ -568,9 +629,7 @@ size_t attention_scratch_bytes(const onela_attention_config &c, bool want_mass) 
 cudaError_t launch_attention(const onela_attention_config &c, AttnParams &p, void *scratch, cudaStream_t s) {
   AttnKind kind;
   plan_call(c, p.mass_out != nullptr, p, static_cast<uint8_t *>(scratch), kind);
-  const int es = c.dtype == ONELA_BF16 ? 2 : 4;
-  const bool vec = (c.d * es) % 16 == 0 && ((reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v)) & 15) == 0;
-  return c.dtype == ONELA_BF16 ? run<__nv_bfloat16>(p, kind, vec, s) : run<float>(p, kind, vec, s);
+  return c.dtype == ONELA_BF16 ? run<__nv_bfloat16>(p, kind, s) : run<float>(p, kind, s);
 }
 
 }  // namespace onela
