@@ -24,7 +24,6 @@ __device__ __forceinline__ void store_f(float *p, float x) { *p = x; }
 __device__ __forceinline__ void store_f(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
 constexpr int kThreads = 128;
-constexpr int kRows = 8;   // query rows per CTA
 constexpr int kToks = 32;  // tokens per step
 
 // N consecutive elements as floats.
@@ -72,39 +71,42 @@ __device__ __forceinline__ void cp_async4_zfill(void *dst, const void *src, uint
 // rows.  K rows are an odd number of 16-byte chunks apart, so that 32 lanes
 // reading the same chunk of 32 rows meet no bank twice.
 struct SimtLayout {
-  int dp, k_stride, v_stride, stage, stages;  // floats of a q row; bytes of a K row, a V row, a stage
-  __host__ __device__ SimtLayout(int d, int es) {
+  int rows, dp, k_stride, v_stride, stage, stages;  // q rows, floats of one; bytes of a K row, a V row, a stage
+  __host__ __device__ SimtLayout(int d, int es, int rows) {
     const int row = (d * es + 15) & ~15;
+    this->rows = rows;
     dp = row / es;
     k_stride = row / 16 % 2 ? row : row + 16;
     v_stride = row;
     stage = kToks * (k_stride + v_stride);
     stages = row <= 256 ? 3 : 2;
   }
-  __host__ __device__ int bytes() const { return kRows * dp * 4 + stages * stage; }
+  __host__ __device__ int bytes() const { return rows * dp * 4 + stages * stage; }
   // CTAs that fit an SM by shared memory, at most 4 (by registers).
   int per_sm() const { return std::min(4, std::max(1, 225 * 1024 / (bytes() + 3 * 1024))); }
 };
 
 // The general kernel: any d, fp32 or bf16.  A CTA takes one part of the
-// prompts, one key-value head and 8 query rows.  Steps of 32 tokens pass
+// prompts, one key-value head and kRows (8, or 4 where there are no more)
+// query rows.  Steps of 32 tokens pass
 // through a ring of stages filled by asynchronous copies of kUnit bytes: 16,
 // or 4 where rows are no multiple of 16 bytes or not on such boundaries; bf16 rows of odd d
 // by plain loads (kUnit = 2).
-// Per step each warp forms two rows' scores (lane = token: a K chunk from
-// shared memory serves two rows, 8 FMAs for 3 loads), takes their softmax by
-// shuffles, and each thread adds to one or two columns of the 8 outputs (one
-// V element for 8 rows).  In fp32 at d = 128 that is about 100 instructions a
+// Per step each warp forms one or two rows' scores (lane = token: a K chunk
+// from shared memory serves both rows, 8 FMAs for 3 loads), takes their softmax by
+// shuffles, and each thread adds to one or two columns of the outputs (one
+// V element for all rows).  In fp32 at d = 128 that is about 100 instructions a
 // token on an SM that can issue 180 in the time the token's rows take to
 // arrive.
-template <typename T, int kUnit>
+template <typename T, int kUnit, int kRows>
 __global__ void __launch_bounds__(kThreads, 4) attn_simt(AttnParams p) {
   extern __shared__ __align__(16) float smem[];
   __shared__ PlanSmem plan;
   __shared__ __align__(16) float ps[kToks][kRows];
   __shared__ __align__(16) float corr[kRows];
   __shared__ __align__(4) uint8_t there[4][4];  // by stage and warp: which of its 8 tokens are there
-  const SimtLayout L(p.d, sizeof(T));
+  const SimtLayout L(p.d, sizeof(T), kRows);
+  constexpr int kOwn = kRows / 4;  // rows whose scores a warp forms
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float *qs = smem;
   uint8_t *ring = reinterpret_cast<uint8_t *>(smem + kRows * L.dp);
@@ -179,11 +181,14 @@ __global__ void __launch_bounds__(kThreads, 4) attn_simt(AttnParams p) {
             (m < p.M && c < p.d) ? to_f(q[((int64_t)r * p.W + w) * p.q_stride + (int64_t)hq * p.d + c]) : 0.f;
     }
 
-    float acc0[kRows], acc1[kRows], mx[2], sum[2];
+    float acc0[kRows], acc1[kRows], mx[kOwn], sum[kOwn];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) acc0[i] = acc1[i] = 0.f;
-    mx[0] = mx[1] = -CUDART_INF_F;
-    sum[0] = sum[1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      mx[i] = -CUDART_INF_F;
+      sum[i] = 0.f;
+    }
 
     for (int i = 0; i < n; ++i) {
       if (L.stages == 3) ptx::cp_async_wait_group1();
@@ -194,10 +199,12 @@ __global__ void __launch_bounds__(kThreads, 4) attn_simt(AttnParams p) {
       const int st = i % L.stages;
       const uint8_t *ks = ring + st * L.stage, *vs = ks + kToks * L.k_stride;
       const uint32_t live = *reinterpret_cast<const uint32_t *>(there[st]);
-      float s[2] = {0.f, 0.f};
+      float s[kOwn];
+#pragma unroll
+      for (int e = 0; e < kOwn; ++e) s[e] = 0.f;
       {
         const uint8_t *kr = ks + lane * L.k_stride;
-        const float *qa = qs + (2 * warp) * L.dp, *qb = qa + L.dp;
+        const float *qa = qs + kOwn * warp * L.dp;
         constexpr int kE = 16 / sizeof(T);
 #pragma unroll 4
         for (int c = 0; c < L.dp; c += kE) {
@@ -205,24 +212,26 @@ __global__ void __launch_bounds__(kThreads, 4) attn_simt(AttnParams p) {
           ldn<kE, true>(reinterpret_cast<const T *>(kr) + c, x);
 #pragma unroll
           for (int e = 0; e < kE; e += 4) {
-            const float4 a = *reinterpret_cast<const float4 *>(qa + c + e), b = *reinterpret_cast<const float4 *>(qb + c + e);
-            s[0] += x[e] * a.x + x[e + 1] * a.y + x[e + 2] * a.z + x[e + 3] * a.w;
-            s[1] += x[e] * b.x + x[e + 1] * b.y + x[e + 2] * b.z + x[e + 3] * b.w;
+#pragma unroll
+            for (int o = 0; o < kOwn; ++o) {
+              const float4 a = *reinterpret_cast<const float4 *>(qa + o * L.dp + c + e);
+              s[o] += x[e] * a.x + x[e + 1] * a.y + x[e + 2] * a.z + x[e + 3] * a.w;
+            }
           }
         }
       }
       const int pos = lo + i * kToks + lane;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int m = m0 + 2 * warp + e;
+      for (int e = 0; e < kOwn; ++e) {
+        const int m = m0 + kOwn * warp + e;
         const float x = (live >> lane) & 1 ? s[e] * p.scale_log2 : -CUDART_INF_F;
         if (p.scores && m < p.M && pos < hi) p.scores[(((int64_t)r * p.Hkv + h) * p.M + m) * p.cap + pos] = x;
         const float mnew = fmaxf(mx[e], warp_max(x));
         const float w = exp2_sub(x, mnew), f = exp2_sub(mx[e], mnew);
         sum[e] = sum[e] * f + warp_sum(w);
         mx[e] = mnew;
-        ps[lane][2 * warp + e] = w;
-        if (lane == 0) corr[2 * warp + e] = f;
+        ps[lane][kOwn * warp + e] = w;
+        if (lane == 0) corr[kOwn * warp + e] = f;
       }
       __syncthreads();
 #pragma unroll
@@ -236,8 +245,8 @@ __global__ void __launch_bounds__(kThreads, 4) attn_simt(AttnParams p) {
         const int step = L.v_stride / (int)sizeof(T);
 #pragma unroll 4
         for (int t = 0; t < nt; ++t) {
-          const float4 a = *reinterpret_cast<const float4 *>(&ps[t][0]), b = *reinterpret_cast<const float4 *>(&ps[t][4]);
-          const float w[kRows] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+          float w[kRows];
+          ldn<kRows, true>(ps[t], w);
           const float x0 = to_f(vc[t * step]);
 #pragma unroll
           for (int e = 0; e < kRows; ++e) acc0[e] += w[e] * x0;
@@ -252,12 +261,13 @@ __global__ void __launch_bounds__(kThreads, 4) attn_simt(AttnParams p) {
     ptx::cp_async_wait_all();
     __syncthreads();
     if (p.direct) {
-      // Sums by row through shared memory (each warp holds two rows').
+      // Sums by row through shared memory (each warp holds its own).
       if (lane == 0) {
-        corr[2 * warp] = sum[0];
-        corr[2 * warp + 1] = sum[1];
-        ps[0][2 * warp] = mx[0];
-        ps[0][2 * warp + 1] = mx[1];
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+          corr[kOwn * warp + i] = sum[i];
+          ps[0][kOwn * warp + i] = mx[i];
+        }
       }
       __syncthreads();
       T *o = static_cast<T *>(p.o);
@@ -283,8 +293,8 @@ __global__ void __launch_bounds__(kThreads, 4) attn_simt(AttnParams p) {
     }
     if (lane == 0) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int m = m0 + 2 * warp + i;
+      for (int i = 0; i < kOwn; ++i) {
+        const int m = m0 + kOwn * warp + i;
         if (m < p.M) p.part_ml[part_row(p, walk.slot, h, m)] = make_float2(mx[i], sum[i]);
       }
     }
@@ -510,8 +520,8 @@ size_t plan_call(const onela_attention_config &c, bool want_mass, AttnParams &p,
   p.q_stride = c.q_stride;
   p.scale_log2 = c.scale * kLog2e;
   const AttnKind kind = choose(c, p);
-  int ctas = SimtLayout(c.d, c.dtype == ONELA_BF16 ? 2 : 4).per_sm() * kAttnSMs;  // that run at once
-  p.rows = kRows;
+  p.rows = p.M <= 4 ? 4 : 8;
+  int ctas = SimtLayout(c.d, c.dtype == ONELA_BF16 ? 2 : 4, p.rows).per_sm() * kAttnSMs;  // that run at once
   p.tile = kToks;
   p.per_slot = 1;
   if (kind == kAttnNarrow) {
@@ -561,11 +571,13 @@ size_t plan_call(const onela_attention_config &c, bool want_mass, AttnParams &p,
   return at;
 }
 
-template <typename T>
+template <typename T, int kRows>
 cudaError_t run_simt(const AttnParams &p, cudaStream_t s) {
-  const size_t smem = (size_t)SimtLayout(p.d, sizeof(T)).bytes();
+  const size_t smem = (size_t)SimtLayout(p.d, sizeof(T), kRows).bytes();
   const uint64_t at = (uint64_t)p.d * sizeof(T) | reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v);
-  auto f = at % 16 == 0 ? attn_simt<T, 16> : at % 4 == 0 ? attn_simt<T, 4> : attn_simt<T, 2>;
+  auto f = at % 16 == 0 ? attn_simt<T, 16, kRows> : attn_simt<T, 4, kRows>;
+  if constexpr (sizeof(T) == 2)
+    if (at % 4) f = attn_simt<T, 2, kRows>;
   const cudaError_t e = ensure_smem_limit((const void *)f, smem);
   if (e != cudaSuccess) return e;
   return launch_kernel(f, (unsigned)((long long)p.parts * p.Hkv * p.row_tiles), kThreads, smem, false, s, p);
@@ -600,7 +612,7 @@ cudaError_t run(const AttnParams &p, AttnKind kind, cudaStream_t s) {
   } else if (kind == kAttnWide) {
     e = launch_attn_wide(p, s);
   } else {
-    e = run_simt<T>(p, s);
+    e = p.rows == 4 ? run_simt<T, 4>(p, s) : run_simt<T, 8>(p, s);
   }
   if (e != cudaSuccess || p.direct) return e;
 
