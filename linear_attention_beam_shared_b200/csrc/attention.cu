@@ -527,7 +527,7 @@ size_t plan_call(const onela_attention_config &c, bool want_mass, AttnParams &p,
   if (kind == kAttnNarrow) {
     p.rows = 16;
     p.tile = 64;
-    ctas = 2 * kAttnSMs;
+    ctas = attn_narrow_ctas(c.d) * kAttnSMs;
   } else if (kind == kAttnWide) {
     p.rows = c.d < 256 && p.M > 128 ? 256 : 128;
     p.tile = 64;

@@ -251,6 +251,19 @@ __device__ __forceinline__ float warp_sum(float x) {
 // exp2(a - b) for a maximum b that may be -inf (nothing seen yet): 0 then.
 __device__ __forceinline__ float exp2_sub(float a, float b) { return b == -CUDART_INF_F ? 0.f : exp2f(a - b); }
 
+// 2^x by the special-function unit (2 ulp); results below 2^-126 become 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+constexpr float kSlack = 8.f;  // growth of a row's maximum, in log2, before the tensor-core kernels rescale its output
+
 constexpr int32_t kStatusPage = 1, kStatusLength = 2;  // ONELA_STATUS_*
 __device__ __forceinline__ void set_status(int32_t *status, int32_t bit) {
   if (status) atomicOr(status, bit);
@@ -259,6 +272,7 @@ __device__ __forceinline__ void set_status(int32_t *status, int32_t bit) {
 // Kernels of a call, chosen on the host.
 enum AttnKind { kAttnSimt = 0, kAttnNarrow = 1, kAttnWide = 2 };
 cudaError_t launch_attn_narrow(const AttnParams &p, cudaStream_t s);  // attention_narrow.cu
+int attn_narrow_ctas(int d);                                           // CTAs of it per SM
 cudaError_t launch_attn_wide(const AttnParams &p, cudaStream_t s);    // attention_wide.cu
 cudaError_t launch_attn_mass_wide(const AttnParams &p, cudaStream_t s);
 

@@ -44,7 +44,6 @@ namespace onela {
 namespace {
 
 constexpr uint64_t kWaitNs = 2000000000ull;  // bound of every wait
-constexpr float kSlack = 8.f;                // growth of the maximum, in log2, before O is rescaled
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 256;  // scores behind the outputs in tensor memory
 constexpr int TT = 64;           // tokens per tile
@@ -84,17 +83,6 @@ struct Maps {
 template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ uint32_t pack(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-// 2^x for x <= kSlack; results below 2^-126 become 0.
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 // Wait unless a wait of this thread has run out before.
 __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, bool &dead) {
@@ -240,7 +228,7 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
             const float a = ex2(fmaf(x[e >> 1][(e & 1) * 16 + 2 * i], p.scale_log2, -off));
             const float bb = ex2(fmaf(x[e >> 1][(e & 1) * 16 + 2 * i + 1], p.scale_log2, -off));
             s4[i & 3] += a + bb;
-            y[i] = pack(a, bb);
+            y[i] = pack_bf16(a, bb);
           }
           ptx::tmem_st<8>(s_t + e * 8, y);
         }
