@@ -587,7 +587,8 @@ ONELA_API int onela_cache_write(const onela_cache_write_config *cfg, const void 
  *   kept         int32 [R][H_kv][keep] or NULL: the kept positions in order, -1
  *                after the n-th.
  * Sources are left as they are: the caller frees their pages.
- *   scratch      at least onela_cache_evict_scratch_bytes(cfg) bytes.
+ *   scratch      at least onela_cache_evict_scratch_bytes(cfg) bytes; not
+ *                used when kept is given.
  * Errors: ONELA_ERR_ARG, ONELA_ERR_SCRATCH, ONELA_ERR_CUDA. */
 typedef struct {
   int32_t R, H_kv, d;

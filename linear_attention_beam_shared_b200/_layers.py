@@ -12,7 +12,6 @@ not given, scratch) is allocated on that stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 
@@ -68,29 +67,32 @@ _CODE = {torch.float32: 0, torch.bfloat16: 1}
 _CODE_OF = {**_CODE, "f32": 0, "bf16": 1}
 _ACT = {"none": ONELA_ACT_NONE, "sigmoid": ONELA_ACT_SIGMOID, "silu": ONELA_ACT_SILU}
 _TORCH = {0: torch.float32, 1: torch.bfloat16}
+_I32, _F32 = torch.int32, torch.float32
 
 
-def _arg(t, name, dtype, shape, device, optional=False):
-    """The pointer of a dense tensor after its checks (None: NULL)."""
-    if t is None:
-        if optional:
-            return None
-        raise TypeError(f"{name} must be a torch.Tensor")
+def _arg(t, name, dtype, shape, index):
+    """The pointer of a dense tensor on device `index` after its checks."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        if t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
+def _opt(t, name, dtype, shape, index):
+    """The same for a tensor that may be None (NULL)."""
+    return None if t is None else _arg(t, name, dtype, shape, index)
+
+
 def _floats(t, name, dim):
-    """dtype code and device of a leading argument, a CUDA fp32 or bf16 tensor of `dim` dimensions."""
+    """dtype code, device index and shape of a leading argument, a CUDA fp32 or
+    bf16 tensor of `dim` dimensions."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -98,16 +100,39 @@ def _floats(t, name, dim):
     code = _CODE.get(t.dtype)
     if code is None:
         raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-    if t.dim() != dim:
-        raise ValueError(f"{name} must have {dim} dimensions, got {t.dim()}")
-    return code, t.device
+    shape = t.shape
+    if len(shape) != dim:
+        raise ValueError(f"{name} must have {dim} dimensions, got {len(shape)}")
+    return code, t.get_device(), shape
 
 
-def _token_stride(t, name):
+def _pool(t, name, H, d):
+    """Shape of a pool [pages][H_kv][page][d] that goes with H and d (None: any)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    shape = t.shape
+    if len(shape) != 4 or (H is not None and shape[1] != H) or shape[3] != d:
+        raise ValueError(f"{name} must be [pages][H_kv][page][d] with matching H_kv and d, got {tuple(shape)}")
+    return shape
+
+
+def _last(t, name, dim):
+    """Entries of a table's rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    shape = t.shape
+    if len(shape) != dim:
+        raise ValueError(f"{name} must have {dim} dimensions, got {len(shape)}")
+    return shape[dim - 1]
+
+
+def _token_stride(t, name, shape):
     """Elements between tokens of [A][B][H][d]: heads dense, tokens evenly spaced."""
-    A, B, H, d = t.shape
-    if t.numel() == 0:
-        raise ValueError(f"{name} must not be empty")
+    A, B, H, d = shape
+    if t.is_contiguous():
+        if A * B * H * d == 0:
+            raise ValueError(f"{name} must not be empty")
+        return H * d
     s = t.stride()
     if (d > 1 and s[3] != 1) or (H > 1 and s[2] != d):
         raise ValueError(f"{name} must be dense within a token")
@@ -117,48 +142,44 @@ def _token_stride(t, name):
     return step
 
 
-def _row_stride(t, name):
-    N, D = t.shape
-    if D > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must be dense within a row")
+def _row_stride(t, name, N, D):
+    if t.is_contiguous():
+        return D
     step = t.stride(0) if N > 1 else D
-    if step < D:
-        raise ValueError(f"{name} must not have overlapping rows")
+    if step < D or (D > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be dense within a row, rows not overlapping")
     return step
 
 
-def _raw_stream(stream, device):
+def _raw_stream(stream, index):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return torch._C._cuda_getCurrentRawStream(index)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _on(stream, device):
-    """The context to allocate in, so that what is allocated belongs to the call's stream."""
+def _empty(shape, dtype, index, stream, like=None):
+    """A new tensor that belongs to the call's stream.  like: a dense tensor of
+    the same shape and type, if there is one (the quicker allocation)."""
     if stream is None:
-        return contextlib.nullcontext()
+        if like is not None:
+            return torch.empty_like(like)
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    return torch.cuda.stream(stream)
-
-
-def _empty(shape, dtype, device, stream):
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with _on(stream, device):
-        return torch.empty(shape, dtype=dtype, device=device)
+        stream = torch.cuda.ExternalStream(int(stream), device=index)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
 
 
 _sizes = {}
 
 
-def _config(key, make, scratch):
+def _config(key, struct, sizes, scratch):
     """(struct, its address, scratch bytes) of a call's sizes."""
     hit = _sizes.get(key)
     if hit is None:
         if len(_sizes) >= 1024:
             _sizes.clear()
-        c = make()
+        c = struct(*sizes)
         at = ctypes.addressof(c)
         hit = _sizes[key] = (c, at, scratch(at) if scratch else 0)
     return hit
@@ -174,57 +195,57 @@ def onela_paged_attention(q, k_pool, v_pool, table, lengths, beam=None, scale=No
     [R][W][row_pages], lengths int32 [R][W]): the beams' own tokens.  mass (in)
     and mass_out fp32 [R][H_kv][row_pages * page]; lse fp32 [R][W][H_q].
     Returns o [R][W][H_q][d]."""
-    code, dev = _floats(q, "q", 4)
+    code, dev, (R, W, H_q, d) = _floats(q, "q", 4)
     dt = q.dtype
-    R, W, H_q, d = q.shape
-    stride = _token_stride(q, "q")
-    if not isinstance(k_pool, torch.Tensor) or k_pool.dim() != 4:
-        raise ValueError("k_pool must be a 4-D tensor [pages][H_kv][page][d]")
-    pool = k_pool.shape
+    stride = _token_stride(q, "q", (R, W, H_q, d))
+    pool = _pool(k_pool, "k_pool", None, d)
     pages, H_kv, page, _ = pool
-    if pool[3] != d or H_kv < 1 or H_q % H_kv:
-        raise ValueError(f"k_pool {tuple(pool)} does not fit q {tuple(q.shape)}")
-    if not isinstance(table, torch.Tensor) or table.dim() != 2:
-        raise ValueError("table must be a 2-D int32 tensor [R][row_pages]")
-    row_pages = table.shape[1]
+    if H_kv < 1 or H_q % H_kv:
+        raise ValueError(f"q's {H_q} heads are no multiple of the cache's {H_kv}")
+    row_pages = _last(table, "table", 2)
     pk = _arg(k_pool, "k_pool", dt, pool, dev)
     pv = _arg(v_pool, "v_pool", dt, pool, dev)
-    pt = _arg(table, "table", torch.int32, (R, row_pages), dev)
-    pl = _arg(lengths, "lengths", torch.int32, (R,), dev)
+    pt = _arg(table, "table", _I32, (R, row_pages), dev)
+    pl = _arg(lengths, "lengths", _I32, (R,), dev)
     bk = bv = bt = bl = None
     bpage = bpages = brow = 0
     if beam is not None:
         tk, tv, tt, tl = beam
-        if not isinstance(tk, torch.Tensor) or tk.dim() != 4 or tk.shape[1] != H_kv or tk.shape[3] != d:
-            raise ValueError("the beams' k_pool must be [pages][H_kv][page][d] with the prompt's H_kv and d")
-        bpages, _, bpage, _ = tk.shape
-        if not isinstance(tt, torch.Tensor) or tt.dim() != 3:
-            raise ValueError("the beams' table must be a 3-D int32 tensor [R][W][row_pages]")
-        brow = tt.shape[2]
-        bk = _arg(tk, "beam k_pool", dt, tk.shape, dev)
-        bv = _arg(tv, "beam v_pool", dt, tk.shape, dev)
-        bt = _arg(tt, "beam table", torch.int32, (R, W, brow), dev)
-        bl = _arg(tl, "beam lengths", torch.int32, (R, W), dev)
+        bpool = _pool(tk, "beam k_pool", H_kv, d)
+        bpages, _, bpage, _ = bpool
+        brow = _last(tt, "beam table", 3)
+        bk = _arg(tk, "beam k_pool", dt, bpool, dev)
+        bv = _arg(tv, "beam v_pool", dt, bpool, dev)
+        bt = _arg(tt, "beam table", _I32, (R, W, brow), dev)
+        bl = _arg(tl, "beam lengths", _I32, (R, W), dev)
         if brow < 1 or bpages < 1 or bpage < 1:
             raise ValueError("the beams' pool and table must not be empty")
-    if mass is not None and mass_out is None:
+    pm = pmo = None
+    if mass_out is not None:
+        cells = (R, H_kv, row_pages * page)
+        pm = _opt(mass, "mass", _F32, cells, dev)
+        pmo = _arg(mass_out, "mass_out", _F32, cells, dev)
+    elif mass is not None:
         raise ValueError("mass needs mass_out")
-    pm = _arg(mass, "mass", torch.float32, (R, H_kv, row_pages * page), dev, True)
-    pmo = _arg(mass_out, "mass_out", torch.float32, (R, H_kv, row_pages * page), dev, True)
-    ps = _arg(lse, "lse", torch.float32, (R, W, H_q), dev, True)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    sizes = (R, W, H_q, H_kv, d, code, kernel, page, pages, row_pages, bpage, bpages, brow, dev.index, stride, scale)
-    want = pmo is not None
-    cfg, at, need = _config(("attention", want, sizes), lambda: onela_attention_config(*sizes),
-                            lambda a: lib.onela_paged_attention_scratch_bytes(a, want))
-    o = _empty((R, W, H_q, d), dt, dev, stream) if out is None else out
-    po = _arg(o, "out", dt, (R, W, H_q, d), dev)
-    if scratch is None:
-        scratch = _empty((max(need, 16),), torch.uint8, dev, stream)
-    px = _arg(scratch, "scratch", torch.uint8, scratch.shape, dev)
-    _check(lib.onela_paged_attention(at, q.data_ptr(), pk, pv, pt, pl, bk, bv, bt, bl, pm, pmo, po, ps, px,
-                                     scratch.numel(), _arg(status, "status", torch.int32, (1,), dev, True),
-                                     _raw_stream(stream, dev)), "onela_paged_attention")
+    sizes = (R, W, H_q, H_kv, d, code, kernel, page, pages, row_pages, bpage, bpages, brow, dev, stride, scale)
+    cfg, at, need = _config(("attention", pmo is None, sizes), onela_attention_config, sizes,
+                            lambda a: lib.onela_paged_attention_scratch_bytes(a, pmo is not None))
+    if out is None:
+        o = _empty((R, W, H_q, d), dt, dev, stream, q if stride == H_q * d and q.is_contiguous() else None)
+        po = o.data_ptr()
+    else:
+        o, po = out, _arg(out, "out", dt, (R, W, H_q, d), dev)
+    px, nbytes = None, 0
+    if scratch is not None:
+        px, nbytes = _arg(scratch, "scratch", torch.uint8, scratch.shape, dev), scratch.numel()
+    elif need:
+        scratch = _empty((need,), torch.uint8, dev, stream)
+        px, nbytes = scratch.data_ptr(), need
+    _check(lib.onela_paged_attention(at, q.data_ptr(), pk, pv, pt, pl, bk, bv, bt, bl, pm, pmo, po,
+                                     _opt(lse, "lse", _F32, (R, W, H_q), dev), px, nbytes,
+                                     _opt(status, "status", _I32, (1,), dev), _raw_stream(stream, dev)),
+           "onela_paged_attention")
     return o
 
 
@@ -240,24 +261,20 @@ def onela_cache_write(k, v, k_pool, v_pool, table, start, counts=None, status=No
     """Write tokens to the cache (see onela.h): k, v [B][n][H_kv][d] (tokens may
     be spaced apart) to positions start[b] + i of table row b; pools
     [pages][H_kv][page][d]; table int32 [B][row_pages]; start, counts int32 [B]."""
-    code, dev = _floats(k, "k", 4)
-    B, n, H_kv, d = k.shape
-    if not isinstance(v, torch.Tensor) or v.shape != k.shape or v.dtype != k.dtype or v.device != dev:
+    code, dev, (B, n, H_kv, d) = _floats(k, "k", 4)
+    dt = k.dtype
+    if not isinstance(v, torch.Tensor) or v.shape != (B, n, H_kv, d) or v.dtype is not dt or v.get_device() != dev:
         raise ValueError("v must match k")
-    ks, vs = _token_stride(k, "k"), _token_stride(v, "v")
-    if not isinstance(k_pool, torch.Tensor) or k_pool.dim() != 4 or k_pool.shape[1] != H_kv or k_pool.shape[3] != d:
-        raise ValueError("k_pool must be [pages][H_kv][page][d] with k's H_kv and d")
-    pool = k_pool.shape
-    if not isinstance(table, torch.Tensor) or table.dim() != 2:
-        raise ValueError("table must be a 2-D int32 tensor [B][row_pages]")
-    row_pages = table.shape[1]
-    sizes = (B, n, H_kv, d, code, pool[2], pool[0], row_pages, dev.index, ks, vs)
-    cfg, at, _ = _config(("write", sizes), lambda: onela_cache_write_config(*sizes), None)
+    pool = _pool(k_pool, "k_pool", H_kv, d)
+    row_pages = _last(table, "table", 2)
+    sizes = (B, n, H_kv, d, code, pool[2], pool[0], row_pages, dev, _token_stride(k, "k", (B, n, H_kv, d)),
+             _token_stride(v, "v", (B, n, H_kv, d)))
+    cfg, at, _ = _config(("write", sizes), onela_cache_write_config, sizes, None)
     _check(lib.onela_cache_write(
-        at, k.data_ptr(), v.data_ptr(), _arg(k_pool, "k_pool", k.dtype, pool, dev),
-        _arg(v_pool, "v_pool", k.dtype, pool, dev), _arg(table, "table", torch.int32, (B, row_pages), dev),
-        _arg(start, "start", torch.int32, (B,), dev), _arg(counts, "counts", torch.int32, (B,), dev, True),
-        _arg(status, "status", torch.int32, (1,), dev, True), _raw_stream(stream, dev)), "onela_cache_write")
+        at, k.data_ptr(), v.data_ptr(), _arg(k_pool, "k_pool", dt, pool, dev), _arg(v_pool, "v_pool", dt, pool, dev),
+        _arg(table, "table", _I32, (B, row_pages), dev), _arg(start, "start", _I32, (B,), dev),
+        _opt(counts, "counts", _I32, (B,), dev), _opt(status, "status", _I32, (1,), dev),
+        _raw_stream(stream, dev)), "onela_cache_write")
 
 
 def onela_cache_evict(k_pool, v_pool, table, lengths, mass, keep, recent, dst_k, dst_v, dst_table, dst_lengths,
@@ -266,33 +283,32 @@ def onela_cache_evict(k_pool, v_pool, table, lengths, mass, keep, recent, dst_k,
     heaviest others, `keep` in all, copied in order to the pages of dst_table
     (see onela.h).  mass fp32 [R][H_kv][row_pages * page]; dst_mass fp32
     [R][H_kv][dst_row_pages * page]; kept int32 [R][H_kv][keep] or None."""
-    code, dev = _floats(k_pool, "k_pool", 4)
-    pool = k_pool.shape
+    code, dev, pool = _floats(k_pool, "k_pool", 4)
+    dt = k_pool.dtype
     pages, H_kv, page, d = pool
-    if not isinstance(dst_k, torch.Tensor) or dst_k.dim() != 4 or dst_k.shape[1:] != pool[1:]:
-        raise ValueError("dst_k must be a pool with k_pool's H_kv, page and d")
-    for t, name in ((table, "table"), (dst_table, "dst_table")):
-        if not isinstance(t, torch.Tensor) or t.dim() != 2:
-            raise ValueError(f"{name} must be a 2-D int32 tensor [R][row_pages]")
-    R, row_pages = table.shape
-    dst_row = dst_table.shape[1]
+    to = _pool(dst_k, "dst_k", H_kv, d)
+    if to[2] != page:
+        raise ValueError("dst_k must have pages of k_pool's size")
+    row_pages, dst_row = _last(table, "table", 2), _last(dst_table, "dst_table", 2)
+    R = table.shape[0]
     keep, recent = int(keep), int(recent)
-    sizes = (R, H_kv, d, code, page, pages, row_pages, dst_k.shape[0], dst_row, keep, recent, dev.index)
-    cfg, at, need = _config(("evict", sizes), lambda: onela_cache_evict_config(*sizes),
-                            lib.onela_cache_evict_scratch_bytes)
-    dt, i32, f32 = k_pool.dtype, torch.int32, torch.float32
-    if scratch is None:
-        scratch = _empty((max(need, 16),), torch.uint8, dev, stream)
+    sizes = (R, H_kv, d, code, page, pages, row_pages, to[0], dst_row, keep, recent, dev)
+    cfg, at, need = _config(("evict", sizes), onela_cache_evict_config, sizes, lib.onela_cache_evict_scratch_bytes)
+    pkept = _opt(kept, "kept", _I32, (R, H_kv, keep), dev)
+    px, nbytes = None, 0
+    if scratch is not None:
+        px, nbytes = _arg(scratch, "scratch", torch.uint8, scratch.shape, dev), scratch.numel()
+    elif pkept is None and need:
+        scratch = _empty((need,), torch.uint8, dev, stream)
+        px, nbytes = scratch.data_ptr(), need
     _check(lib.onela_cache_evict(
         at, _arg(k_pool, "k_pool", dt, pool, dev), _arg(v_pool, "v_pool", dt, pool, dev),
-        _arg(table, "table", i32, (R, row_pages), dev), _arg(lengths, "lengths", i32, (R,), dev),
-        _arg(mass, "mass", f32, (R, H_kv, row_pages * page), dev), _arg(dst_k, "dst_k", dt, dst_k.shape, dev),
-        _arg(dst_v, "dst_v", dt, dst_k.shape, dev), _arg(dst_table, "dst_table", i32, (R, dst_row), dev),
-        _arg(dst_lengths, "dst_lengths", i32, (R,), dev),
-        _arg(dst_mass, "dst_mass", f32, (R, H_kv, dst_row * page), dev),
-        _arg(kept, "kept", i32, (R, H_kv, keep), dev, True),
-        _arg(scratch, "scratch", torch.uint8, scratch.shape, dev), scratch.numel(),
-        _arg(status, "status", i32, (1,), dev, True), _raw_stream(stream, dev)), "onela_cache_evict")
+        _arg(table, "table", _I32, (R, row_pages), dev), _arg(lengths, "lengths", _I32, (R,), dev),
+        _arg(mass, "mass", _F32, (R, H_kv, row_pages * page), dev), _arg(dst_k, "dst_k", dt, to, dev),
+        _arg(dst_v, "dst_v", dt, to, dev), _arg(dst_table, "dst_table", _I32, (R, dst_row), dev),
+        _arg(dst_lengths, "dst_lengths", _I32, (R,), dev),
+        _arg(dst_mass, "dst_mass", _F32, (R, H_kv, dst_row * page), dev), pkept, px, nbytes,
+        _opt(status, "status", _I32, (1,), dev), _raw_stream(stream, dev)), "onela_cache_evict")
 
 
 def onela_block_norm(y=None, x=None, gate=None, gate_act="none", w_post=None, scale=None, alpha=1.0, w_pre=None,
@@ -306,44 +322,61 @@ def onela_block_norm(y=None, x=None, gate=None, gate_act="none", w_post=None, sc
     lead = y if y is not None else x
     if lead is None:
         raise ValueError("give y, x or both")
-    ycode, dev = _floats(lead, "y" if y is not None else "x", 2)
-    N, D = lead.shape
-    for t in (x, gate):
-        if t is not None and dtype is None:
-            dtype = t.dtype
-    code = _CODE_OF.get(dtype if dtype is not None else lead.dtype)
+    ycode, dev, (N, D) = _floats(lead, "y" if y is not None else "x", 2)
+    if dtype is None:
+        dtype = x.dtype if x is not None else gate.dtype if gate is not None else lead.dtype
+    code = _CODE_OF.get(dtype)
     if code is None:
         raise ValueError("dtype must be f32 or bf16")
     dt = _TORCH[code]
-    if gate_act not in _ACT:
+    act = _ACT.get(gate_act)
+    if act is None:
         raise ValueError(f"gate_act must be one of {sorted(_ACT)}")
-    act = _ACT[gate_act]
     if (gate is None) != (act == ONELA_ACT_NONE):
         raise ValueError("gate and gate_act go together")
-    strides, ptrs = [], []
-    for t, name, want in ((y, "y", None), (gate, "gate", dt), (x, "x", dt)):
-        if t is None:
-            strides.append(D)
-            ptrs.append(None)
-            continue
-        if t.device != dev or t.shape != lead.shape or (want is not None and t.dtype != want):
-            raise ValueError(f"{name} must be {want or 'float32 or bfloat16'} {tuple(lead.shape)} on {dev}")
-        strides.append(_row_stride(t, name))
-        ptrs.append(t.data_ptr())
-    f32 = torch.float32
-    group = D
+    py = pg = px = None
+    sy = sg = sx = D
+    like = None  # a dense tensor of the outputs' shape and type
+    if y is not None:
+        py, sy = y.data_ptr(), _row_stride(y, "y", N, D)
+        if ycode == code and y.is_contiguous():
+            like = y
+    if gate is not None:
+        pg, sg = _plane(gate, "gate", dt, N, D, dev), _row_stride(gate, "gate", N, D)
+        if gate.is_contiguous():
+            like = gate
+    if x is not None:
+        px, sx = _plane(x, "x", dt, N, D, dev), _row_stride(x, "x", N, D)
+        if x.is_contiguous():
+            like = x
+    group, pw = D, None
     if w_post is not None:
-        if not isinstance(w_post, torch.Tensor) or w_post.dim() != 1 or not w_post.numel() or D % w_post.numel():
+        group = _last(w_post, "w_post", 1)
+        if group < 1 or D % group:
             raise ValueError("w_post must be a vector whose length divides D")
-        group = w_post.numel()
-    sizes = (N, *strides, D, group, ycode if y is not None else code, code, act, dev.index, float(alpha), float(eps))
-    cfg, at, _ = _config(("norm", sizes), lambda: onela_block_norm_config(*sizes), None)
-    if x_out is None and want_x:
-        x_out = _empty((N, D), dt, dev, stream)
-    if n_out is None and w_pre is not None:
-        n_out = _empty((N, D), dt, dev, stream)
-    _check(lib.onela_block_norm(
-        at, *ptrs, _arg(w_post, "w_post", f32, (group,), dev, True), _arg(scale, "scale", f32, (D,), dev, True),
-        _arg(w_pre, "w_pre", f32, (D,), dev, True), _arg(x_out, "x_out", dt, (N, D), dev, True),
-        _arg(n_out, "n_out", dt, (N, D), dev, True), _raw_stream(stream, dev)), "onela_block_norm")
+        pw = _arg(w_post, "w_post", _F32, (group,), dev)
+    sizes = (N, sy, sg, sx, D, group, ycode if y is not None else code, code, act, dev, float(alpha), float(eps))
+    cfg, at, _ = _config(("norm", sizes), onela_block_norm_config, sizes, None)
+    pxo = pno = None
+    if x_out is not None:
+        pxo = _arg(x_out, "x_out", dt, (N, D), dev)
+    elif want_x:
+        x_out = _empty((N, D), dt, dev, stream, like)
+        pxo = x_out.data_ptr()
+    if n_out is not None:
+        pno = _arg(n_out, "n_out", dt, (N, D), dev)
+    elif w_pre is not None:
+        n_out = _empty((N, D), dt, dev, stream, like)
+        pno = n_out.data_ptr()
+    _check(lib.onela_block_norm(at, py, pg, px, pw, _opt(scale, "scale", _F32, (D,), dev),
+                                _opt(w_pre, "w_pre", _F32, (D,), dev), pxo, pno, _raw_stream(stream, dev)),
+           "onela_block_norm")
     return x_out, n_out
+
+
+def _plane(t, name, dt, N, D, index):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != index or t.dtype is not dt or t.shape != (N, D):
+        raise ValueError(f"{name} must be {dt} {(N, D)} on cuda:{index}")
+    return t.data_ptr()

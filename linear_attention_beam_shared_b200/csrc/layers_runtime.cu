@@ -180,7 +180,7 @@ int onela_cache_evict(const onela_cache_evict_config *cfg, const void *k_pool, c
                       const int32_t *dst_table, int32_t *dst_lengths, float *dst_mass, int32_t *kept, void *scratch,
                       size_t scratch_bytes, int32_t *status, onela_stream stream) {
   if (!cfg || !k_pool || !v_pool || !table || !lengths || !mass || !dst_k || !dst_v || !dst_table || !dst_lengths ||
-      !dst_mass || !scratch)
+      !dst_mass || (!kept && !scratch))
     return ONELA_ERR_ARG;
   const onela_cache_evict_config c = *cfg;
   if (!valid_evict(c)) return ONELA_ERR_ARG;
@@ -192,8 +192,10 @@ int onela_cache_evict(const onela_cache_evict_config *cfg, const void *k_pool, c
   for (const void *x : {(const void *)table, (const void *)lengths, (const void *)mass, (const void *)dst_table,
                         (const void *)dst_lengths, (const void *)dst_mass, (const void *)kept, (const void *)status})
     if (!aligned(x, 4)) return ONELA_ERR_ARG;
-  if (!aligned(scratch, 256)) return ONELA_ERR_ARG;
-  if (scratch_bytes < onela_cache_evict_scratch_bytes(&c)) return ONELA_ERR_SCRATCH;
+  if (!kept) {
+    if (!aligned(scratch, 256)) return ONELA_ERR_ARG;
+    if (scratch_bytes < onela_cache_evict_scratch_bytes(&c)) return ONELA_ERR_SCRATCH;
+  }
   onela::CacheEvictParams p = {};
   p.R = c.R;
   p.Hkv = c.H_kv;
