@@ -473,18 +473,41 @@ __global__ void __launch_bounds__(kWpr == 1 ? 128 : kWpr * 32) attn_join(AttnPar
 }
 
 // The weight each prompt position drew, from the scores the split kernel
-// stored: a thread per position adds exp2(s - lse2) over the M rows in order.
+// stored: a thread takes four positions (kP; one where rows are no multiple
+// of 4) and adds exp2(s - lse2) over the M rows in order.
+template <int kP>
 __global__ void __launch_bounds__(kThreads) attn_mass(AttnParams p) {
-  const int chunks = (p.cap + kThreads - 1) / kThreads;
-  const int pos = (blockIdx.x % chunks) * kThreads + threadIdx.x;
+  const int chunks = (p.cap + kThreads * kP - 1) / (kThreads * kP);
+  const int pos = ((blockIdx.x % chunks) * kThreads + threadIdx.x) * kP;
   const int rh = blockIdx.x / chunks, r = rh / p.Hkv;
+  const int len = prompt_len(p, r);
   ptx::pdl_wait();
-  if (pos >= prompt_len(p, r)) return;
+  if (pos >= len) return;
   const float *l2 = p.lse2 + (int64_t)rh * p.M, *sc = p.scores + (int64_t)rh * p.M * p.cap + pos;
-  float t = 0.f;
-  for (int m = 0; m < p.M; ++m) t += exp2_sub(sc[(int64_t)m * p.cap], l2[m]);
+  float t[kP];
+#pragma unroll
+  for (int i = 0; i < kP; ++i) t[i] = 0.f;
+#pragma unroll 4
+  for (int m = 0; m < p.M; ++m) {
+    float x[kP];
+    ldn<kP, true>(sc + (int64_t)m * p.cap, x);
+    const float l = l2[m];
+#pragma unroll
+    for (int i = 0; i < kP; ++i) t[i] += exp2_sub(x[i], l);
+  }
   const int64_t at = (int64_t)rh * p.cap + pos;
-  p.mass_out[at] = p.mass ? p.mass[at] + t : t;
+  if (kP == 4 && pos + 4 <= len) {
+    float4 o = make_float4(t[0], t[1], t[2], t[kP - 1]);
+    if (p.mass) {
+      const float4 a = *reinterpret_cast<const float4 *>(p.mass + at);
+      o = make_float4(o.x + a.x, o.y + a.y, o.z + a.z, o.w + a.w);
+    }
+    *reinterpret_cast<float4 *>(p.mass_out + at) = o;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kP; ++i)
+      if (pos + i < len) p.mass_out[at + i] = p.mass ? p.mass[at + i] + t[i] : t[i];
+  }
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -619,8 +642,11 @@ cudaError_t run(const AttnParams &p, AttnKind kind, cudaStream_t s) {
   e = run_join<T>(p, s);
   if (e != cudaSuccess || !p.mass_out) return e;
   if (kind == kAttnWide) return launch_attn_mass_wide(p, s);
-  return launch_kernel(attn_mass, (unsigned)((long long)p.R * p.Hkv * ((p.cap + kThreads - 1) / kThreads)), kThreads, 0, true,
-                s, p);
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p.mass) | reinterpret_cast<uintptr_t>(p.mass_out);
+  const int per = p.cap % 4 == 0 && (at & 15) == 0 ? 4 : 1;
+  const unsigned grid = (unsigned)((long long)p.R * p.Hkv * ((p.cap + kThreads * per - 1) / (kThreads * per)));
+  return per == 4 ? launch_kernel(attn_mass<4>, grid, kThreads, 0, true, s, p)
+                  : launch_kernel(attn_mass<1>, grid, kThreads, 0, true, s, p);
 }
 
 }  // namespace
