@@ -28,6 +28,37 @@ __device__ __forceinline__ void st(void *p, int64_t i, float x, int bf16) {
   else static_cast<float *>(p)[i] = x;
 }
 
+// Two floats in one register pair: the packed fp32 instructions of sm_100 take
+// two products or sums in one issue slot, each rounded as its scalar form.
+struct F2 {
+  uint64_t u;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.u) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 un(F2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x.u));
+  return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
+  return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.u) : "l"(a.u), "l"(b.u), "l"(c.u));
+  return r;
+}
+
 // Eight consecutive elements, 16-byte aligned, as they lie in memory and as floats.
 template <bool kBf>
 struct Vec;
@@ -37,19 +68,19 @@ struct Vec<true> {
   __device__ __forceinline__ void load(const void *p, int64_t i) {
     u = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p) + i));
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
+  __device__ __forceinline__ void get(F2 (&v)[4]) const {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[2 * e] = __uint_as_float(w[e] << 16);
-      v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-    }
+    for (int e = 0; e < 4; ++e) v[e] = f2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
   }
-  static __device__ __forceinline__ void store(void *p, int64_t i, const float (&v)[8]) {
-    union { uint4 u; __nv_bfloat162 h[4]; } a;
+  static __device__ __forceinline__ void store(void *p, int64_t i, const F2 (&v)[4]) {
+    uint32_t w[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) a.h[e] = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p) + i) = a.u;
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = un(v[e]);
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(f.y), "f"(f.x));
+    }
+    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
 template <>
@@ -60,20 +91,25 @@ struct Vec<false> {
     a = __ldcs(q);
     b = __ldcs(q + 1);
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  __device__ __forceinline__ void get(F2 (&v)[4]) const {
+    v[0] = f2(a.x, a.y);
+    v[1] = f2(a.z, a.w);
+    v[2] = f2(b.x, b.y);
+    v[3] = f2(b.z, b.w);
   }
-  static __device__ __forceinline__ void store(void *p, int64_t i, const float (&v)[8]) {
+  static __device__ __forceinline__ void store(void *p, int64_t i, const F2 (&v)[4]) {
     float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
-    q[0] = make_float4(v[0], v[1], v[2], v[3]);
-    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+    const float2 c = un(v[0]), d = un(v[1]), e = un(v[2]), f = un(v[3]);
+    q[0] = make_float4(c.x, c.y, d.x, d.y);
+    q[1] = make_float4(e.x, e.y, f.x, f.y);
   }
 };
-__device__ __forceinline__ void weights8(const float *p, float (&v)[8]) {
+__device__ __forceinline__ void weights8(const float *p, F2 (&v)[4]) {
   const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  v[0] = f2(a.x, a.y);
+  v[1] = f2(a.z, a.w);
+  v[2] = f2(b.x, b.y);
+  v[3] = f2(b.z, b.w);
 }
 
 // 1 / (1 + exp(-z)) by the special-function unit: exp2 within 2 ulp, the
@@ -84,6 +120,16 @@ __device__ __forceinline__ float sigmoid(float z) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   return r;
+}
+__device__ __forceinline__ F2 sigmoid2(F2 z) {
+  const float2 t = un(z * f2(-1.4426950408889634f, -1.4426950408889634f));
+  float2 e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  e = un(f2(e.x, e.y) + f2(1.f, 1.f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(e.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(e.y));
+  return f2(e.x, e.y);
 }
 __device__ __forceinline__ float act(float z, int kind) {
   return kind == ONELA_ACT_SILU ? z * sigmoid(z) : sigmoid(z);
@@ -115,41 +161,45 @@ __device__ __forceinline__ float block_sum(float x, float (&red)[2][32], int &n)
 // the next row is loaded before this one is reduced, so that loads are always
 // under way.  kLoop = false: a row per CTA, weights from global memory (few rows:
 // latency is what counts, and nothing would be reused).
-template <bool kYBf, bool kBf, int kV, bool kLoop, int kMaxThreads = 512>
-__global__ void __launch_bounds__(kMaxThreads, kV == 4 ? 1 : 2) block_norm_vec(BlockNormParams p) {
+// kAll: y, gate, x, w_post over the whole row, w_pre and x_out are all there
+// (the sandwich norm in full), so that nothing is asked at run time.
+template <bool kYBf, bool kBf, int kV, bool kLoop, bool kAll = false, int kMaxThreads = 512>
+__global__ void __launch_bounds__(kMaxThreads, kV == 4 || (kV == 2 && !kLoop) ? 1 : 2) block_norm_vec(const __grid_constant__ BlockNormParams p) {
   // kLoop: [D] factor of u, [D] w_pre; then, for group norms that do not fit a warp, [D / 8] sums.
   extern __shared__ __align__(16) float sm[];
   __shared__ __align__(16) float red[2][32];
   int sums = 0;
   const int tid = threadIdx.x, nt = blockDim.x, nv = p.D / 8, gv = p.group / 8;
   if (tid < 64) red[tid >> 5][tid & 31] = 0.f;
-  __syncthreads();
+  const bool has_y = kAll || p.y, has_g = kAll || p.gate, has_x = kAll || p.x, has_post = kAll || p.w_post;
+  const bool has_pre = kAll || p.w_pre, has_out = kAll || p.x_out, whole = kAll || p.group == p.D;
   float *fac = sm, *wpre = sm + p.D, *gsum = kLoop ? sm + 2 * p.D : sm;
   const bool in_warp = gv <= 32 && (gv & (gv - 1)) == 0;  // a group is an aligned power of two of lanes
-  auto factor = [&](int c, float (&w)[8]) {               // of u at vector c: w_post * alpha * scale
-    if (p.w_post) weights8(p.w_post + (8 * c) % p.group, w);
-    else
+  auto factor = [&](int c, F2 (&w)[4]) {                  // of u at vector c: w_post * alpha * scale
+    if (has_post) {
+      weights8(p.w_post + (8 * c) % p.group, w);
+    } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = 1.f;
-    float z[8];
+      for (int i = 0; i < 4; ++i) w[i] = f2(1.f, 1.f);
+    }
+    F2 z[4];
+    const F2 al = f2(p.alpha, p.alpha);
     if (p.scale) weights8(p.scale + 8 * c, z);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] *= p.scale ? p.alpha * z[i] : p.alpha;
+    for (int i = 0; i < 4; ++i) w[i] = w[i] * (p.scale ? al * z[i] : al);
   };
   if (kLoop) {
     for (int c = tid; c < nv; c += nt) {
-      float w[8];
+      F2 w[4];
       factor(c, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) fac[8 * c + i] = w[i];
-      if (p.w_pre) {
+      Vec<false>::store(fac, 8 * c, w);
+      if (has_pre) {
         weights8(p.w_pre + 8 * c, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) wpre[8 * c + i] = w[i];
+        Vec<false>::store(wpre, 8 * c, w);
       }
     }
-    __syncthreads();
   }
+  __syncthreads();
   Vec<kYBf> y[kV];
   Vec<kBf> x[kV], g[kV];
   auto fetch = [&](int64_t row) {
@@ -157,32 +207,35 @@ __global__ void __launch_bounds__(kMaxThreads, kV == 4 ? 1 : 2) block_norm_vec(B
     for (int e = 0; e < kV; ++e) {
       const int c = tid + e * nt;
       if (c < nv) {
-        if (p.y) y[e].load(p.y, row * p.y_stride + 8 * c);
-        if (p.gate) g[e].load(p.gate, row * p.gate_stride + 8 * c);
-        if (p.x) x[e].load(p.x, row * p.x_stride + 8 * c);
+        if (has_y) y[e].load(p.y, row * p.y_stride + 8 * c);
+        if (has_g) g[e].load(p.gate, row * p.gate_stride + 8 * c);
+        if (has_x) x[e].load(p.x, row * p.x_stride + 8 * c);
       }
     }
   };
   int64_t row = blockIdx.x;
   fetch(row);
   for (;;) {
-    float v[kV][8];  // y, then x'
+    F2 v[kV][4];  // y, then x'
     float inv[kV];
-    if (p.y) {
+    if (has_y) {
       float sq[kV], s = 0.f;
 #pragma unroll
       for (int e = 0; e < kV; ++e) {
         sq[e] = 0.f;
         if (tid + e * nt < nv) {
           y[e].get(v[e]);
+          F2 t = v[e][0] * v[e][0];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sq[e] += v[e][i] * v[e][i];
+          for (int i = 1; i < 4; ++i) t = fma2(v[e][i], v[e][i], t);
+          const float2 f = un(t);
+          sq[e] = f.x + f.y;
         }
         s += sq[e];
         inv[e] = 1.f;
       }
-      if (p.w_post) {
-        if (p.group == p.D) {
+      if (has_post) {
+        if (whole) {
           const float t = rsqrtf(block_sum(s, red, sums) / (float)p.D + p.eps);
 #pragma unroll
           for (int e = 0; e < kV; ++e) inv[e] = t;
@@ -210,51 +263,54 @@ __global__ void __launch_bounds__(kMaxThreads, kV == 4 ? 1 : 2) block_norm_vec(B
         }
       }
     }
-    float s = 0.f;
+    F2 s2 = f2(0.f, 0.f);
 #pragma unroll
     for (int e = 0; e < kV; ++e) {
       const int c = tid + e * nt;
       if (c >= nv) continue;
-      float z[8];
-      if (p.y) {
-        float w[8];
+      F2 z[4];
+      if (has_y) {
+        F2 w[4];
         if (kLoop) weights8(fac + 8 * c, w);
         else factor(c, w);
+        const F2 iv = f2(inv[e], inv[e]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[e][i] *= inv[e] * w[i];
-        if (p.gate) {
+        for (int i = 0; i < 4; ++i) v[e][i] = v[e][i] * (iv * w[i]);
+        if (has_g) {
           g[e].get(z);
           if (p.act == ONELA_ACT_SILU) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[e][i] *= z[i];
+            for (int i = 0; i < 4; ++i) v[e][i] = v[e][i] * z[i];
           }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[e][i] *= sigmoid(z[i]);
+          for (int i = 0; i < 4; ++i) v[e][i] = v[e][i] * sigmoid2(z[i]);
         }
-        if (p.x) {
+        if (has_x) {
           x[e].get(z);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[e][i] += z[i];
+          for (int i = 0; i < 4; ++i) v[e][i] = v[e][i] + z[i];
         }
       } else {
         x[e].get(v[e]);
       }
-      if (p.x_out) Vec<kBf>::store(p.x_out, row * p.D + 8 * c, v[e]);
+      if (has_out) Vec<kBf>::store(p.x_out, row * p.D + 8 * c, v[e]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += v[e][i] * v[e][i];
+      for (int i = 0; i < 4; ++i) s2 = fma2(v[e][i], v[e][i], s2);
     }
     const int64_t next = row + gridDim.x;
     if (kLoop && next < p.N) fetch(next);
-    if (p.w_pre) {
-      const float t = rsqrtf(block_sum(s, red, sums) / (float)p.D + p.eps);
+    if (has_pre) {
+      const float2 f = un(s2);
+      const float t = rsqrtf(block_sum(f.x + f.y, red, sums) / (float)p.D + p.eps);
+      const F2 tv = f2(t, t);
 #pragma unroll
       for (int e = 0; e < kV; ++e) {
         const int c = tid + e * nt;
         if (c >= nv) continue;
-        float w[8];
+        F2 w[4];
         weights8(kLoop ? wpre + 8 * c : p.w_pre + 8 * c, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] *= v[e][i] * t;
+        for (int i = 0; i < 4; ++i) w[i] = w[i] * (v[e][i] * tv);
         Vec<kBf>::store(p.n_out, row * p.D + 8 * c, w);
       }
     }
@@ -322,7 +378,7 @@ cudaError_t run_vec(const BlockNormParams &p, int threads, cudaStream_t s) {
   const int gv = p.group / 8;
   const bool sums = p.y && p.w_post && p.group != p.D && !(gv <= 32 && (gv & (gv - 1)) == 0);
   const size_t gs = sums ? (size_t)p.D / 8 * 4 : 0;
-  block_norm_vec<kYBf, kBf, kV, false, kMaxThreads><<<(unsigned)p.N, threads, gs, s>>>(p);
+  block_norm_vec<kYBf, kBf, kV, false, false, kMaxThreads><<<(unsigned)p.N, threads, gs, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -335,7 +391,8 @@ bool run_loop(const BlockNormParams &p, int threads, cudaStream_t s, cudaError_t
   const int per_sm = std::max(1, std::min(std::min(1024 / threads, 32), (int)(200 * 1024 / (smem + 1024))));
   const int64_t ctas = (int64_t)kSMs * per_sm;
   if (p.N < 4 * ctas) return false;
-  auto f = block_norm_vec<kYBf, kBf, kV, true>;
+  const bool all = p.y && p.gate && p.x && p.w_post && p.group == p.D && p.w_pre && p.x_out;
+  auto f = all ? block_norm_vec<kYBf, kBf, kV, true, true> : block_norm_vec<kYBf, kBf, kV, true, false>;
   e = ensure_smem_limit((const void *)f, smem);
   if (e == cudaSuccess) {
     f<<<(unsigned)ctas, threads, smem, s>>>(p);
@@ -349,8 +406,10 @@ cudaError_t run_types(const BlockNormParams &p, cudaStream_t s) {
   const int nv = p.D / 8;
   auto threads = [nv](int per) { return ((nv + per - 1) / per + 31) / 32 * 32; };
   cudaError_t e;
-  // Looping, two vectors a thread from 256 vectors on: fewer warps to wait for at a sum.
-  if (nv <= 256 ? run_loop<kYBf, kBf, 1>(p, threads(1), s, e) : nv <= 1024 && run_loop<kYBf, kBf, 2>(p, threads(2), s, e))
+  // Looping, two vectors a thread from 256 vectors on: fewer warps to wait for
+  // at a sum (20480 rows of 4096 in bf16: 174 us with one, 156 with two).  fp32 rows
+  // in flight take twice the registers: one vector up to 512.
+  if (nv <= (kYBf && kBf ? 256 : 512) ? run_loop<kYBf, kBf, 1>(p, threads(1), s, e) : nv <= 1024 && run_loop<kYBf, kBf, 2>(p, threads(2), s, e))
     return e;
   if (nv <= 512) return run_vec<kYBf, kBf, 1>(p, threads(1), s);
   if (nv <= 1024) return run_vec<kYBf, kBf, 2>(p, threads(2), s);
