@@ -113,6 +113,7 @@ __global__ void __launch_bounds__(kThreads, 4) attn_simt(AttnParams p) {
 
   const int rt = blockIdx.x % p.row_tiles, uh = blockIdx.x / p.row_tiles;
   const int h = uh % p.Hkv;
+  ptx::pdl_wait();
   ptx::pdl_launch_dependents();
   PlanWalk walk;
   walk.begin<kThreads>(p, plan, uh / p.Hkv);
@@ -301,171 +302,227 @@ __global__ void __launch_bounds__(kThreads, 4) attn_simt(AttnParams p) {
   }
 }
 
-// A lane's columns of a row of d: with kD (64, 128 or 256) known, kD / 32
-// consecutive ones; otherwise columns lane + 32 i.
-template <int kD>
+// A row of d over a group of lanes, as loaded and as floats: with kD (64, 128
+// or 256) known, 8 consecutive columns for each of kD / 8 lanes; otherwise
+// columns lane + 32 i of the whole warp.
+template <typename T, int kD>
 struct Cols {
-  static constexpr int kN = kD ? kD / 32 : 8;
-  template <typename T>
-  static __device__ __forceinline__ void load(const T *row, int lane, int d, float (&v)[kN]) {
-    if constexpr (kD) {
-      ldn<kN, true>(row + lane * kN, v);
-    } else {
+  static constexpr int kLanes = kD ? kD / 8 : 32;
+  uint4 u[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T *row, int gl, int) {
 #pragma unroll
-      for (int i = 0; i < kN; ++i) v[i] = lane + 32 * i < d ? to_f(row[lane + 32 * i]) : 0.f;
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = reinterpret_cast<const uint4 *>(row + gl * 8)[i];
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+      const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(T) == 2) {
+          v[2 * e] = __uint_as_float(w[e] << 16);
+          v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+        } else {
+          v[4 * i + e] = __uint_as_float(w[e]);
+        }
+      }
     }
   }
-  template <typename T>
-  static __device__ __forceinline__ void store(T *row, int lane, int d, const float (&v)[kN]) {
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int c = kD ? lane * kN + i : lane + 32 * i;
-      if (kD || c < d) store_f(row + c, v[i]);
+  static __device__ __forceinline__ void store(T *row, int gl, int, const float (&v)[8]) {
+    if constexpr (sizeof(T) == 2) {
+      *reinterpret_cast<uint4 *>(row + gl * 8) =
+          make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    } else {
+      reinterpret_cast<float4 *>(row + gl * 8)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4 *>(row + gl * 8)[1] = make_float4(v[4], v[5], v[6], v[7]);
     }
   }
 };
+template <typename T>
+struct Cols<T, 0> {
+  static constexpr int kLanes = 32;
+  float f[8];
+  __device__ __forceinline__ void load(const T *row, int gl, int d) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = gl + 32 * i < d ? to_f(row[gl + 32 * i]) : 0.f;
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = 0.f;
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = f[i];
+  }
+  static __device__ __forceinline__ void store(T *row, int gl, int d, const float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (gl + 32 * i < d) store_f(row + gl + 32 * i, v[i]);
+  }
+};
 
-// Joins a row's pieces and the beam's own tokens.  kWpr warps share a query
-// row: 1 when there are rows enough to fill the SMs, 8 when a few rows have
-// many pieces (64 rows of 18 pieces: 8 warps halve the time).  The beams' own tokens are few
-// (a decode horizon) and differ from beam to beam, so their scores are formed
-// here by the warp, four tokens at a time.
+// Joins a row's pieces and the beam's own tokens.  A query row takes a group
+// of lanes (8, 16 or 32 for d = 64, 128, 256: 16 bytes of bf16 a lane), so
+// that a warp reads a beam's K and V once for several heads of a group.  kWpr
+// warps share those rows: 1 when there are rows enough to fill the SMs, 8 when
+// a few rows have many pieces (64 rows of 18 pieces: half the time).  The
+// beams' own tokens are few (a decode horizon) and differ from beam to beam,
+// so their scores are formed here, four tokens at a time.
 template <typename T, int kD, int kWpr>
-__global__ void __launch_bounds__(kWpr == 1 ? 128 : kWpr * 32) attn_join(AttnParams p) {
-  constexpr int kBlock = kWpr == 1 ? 128 : kWpr * 32, kRowsPer = kBlock / 32 / kWpr;
-  using C = Cols<kD>;
-  constexpr int N = C::kN;
+__global__ void __launch_bounds__(kWpr == 1 ? 128 : kWpr * 32, kWpr == 1 ? 5 : 2)
+    attn_join(const __grid_constant__ AttnParams p) {
+  using C = Cols<T, kD>;
+  constexpr int kBlock = kWpr == 1 ? 128 : kWpr * 32, kL = C::kLanes;
+  constexpr int kRpw = 32 / kL, kRowsPer = kRpw * (kWpr == 1 ? 4 : 1);
   __shared__ PlanSmem plan;
-  __shared__ float2 wml[kWpr];
+  __shared__ float2 wml[kWpr][kRpw];
   __shared__ float wacc[kWpr == 1 ? 1 : kWpr][kWpr == 1 ? 1 : 256];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gl = lane % kL, grp = lane / kL;
   const int part = kWpr == 1 ? 0 : warp;
-  const int rows = p.W * p.Hq, groups = (rows + kRowsPer - 1) / kRowsPer;
-  const int r = blockIdx.x / groups, row = (blockIdx.x % groups) * kRowsPer + (kWpr == 1 ? warp : 0);
+  const int rows = p.W * p.Hq, blocks = (rows + kRowsPer - 1) / kRowsPer;
+  const int r = blockIdx.x / blocks;
+  const int want = (blockIdx.x % blocks) * kRowsPer + (kWpr == 1 ? warp * kRpw : 0) + grp, row = min(want, rows - 1);
   int off, pieces;
   plan_row<kBlock>(p, plan, r, off, pieces);
   off *= p.per_slot;
   pieces *= p.per_slot;
-  if (row == 0 && part == 0 && lane == 0 && p.lengths[r] != prompt_len(p, r)) set_status(p.status, kStatusLength);
-  const bool live = row < rows;
-  const int w = live ? row / p.Hq : 0, hq = live ? row % p.Hq : 0, h = hq / p.G, m = w * p.G + hq % p.G;
-
-  float acc[N], mx = -CUDART_INF_F, sum = 0.f;
+  if (blockIdx.x % blocks == 0 && threadIdx.x == 0 && p.lengths[r] != prompt_len(p, r)) set_status(p.status, kStatusLength);
+  const int w = row / p.Hq, hq = row % p.Hq, h = hq / p.G, m = w * p.G + hq % p.G;
+  auto group_sum = [](float x) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) acc[i] = 0.f;
+    for (int o = kL / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+  };
+
+  float acc[8], mx = -CUDART_INF_F, sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
   // The beam's own tokens first: nothing of them comes from the split kernel,
   // which may still be running.
-  if (p.bk && live) {
+  if (p.bk) {
     const T *bk = static_cast<const T *>(p.bk), *bv = static_cast<const T *>(p.bv);
-    float qv[N];
-    C::load(static_cast<const T *>(p.q) + ((int64_t)r * p.W + w) * p.q_stride + (int64_t)hq * p.d, lane, p.d, qv);
+    C qr;
+    qr.load(static_cast<const T *>(p.q) + ((int64_t)r * p.W + w) * p.q_stride + (int64_t)hq * p.d, gl, p.d);
     const int bcap = p.brow_pages * p.bpage, given = p.blengths[(int64_t)r * p.W + w];
-    const int n = given < 0 ? 0 : (given > bcap ? bcap : given);
-    if (n != given && lane == 0) set_status(p.status, kStatusLength);
+    const int n = given < 0 ? 0 : (given > bcap ? bcap : given), most = __reduce_max_sync(0xffffffffu, n);
+    if (n != given && gl == 0) set_status(p.status, kStatusLength);
     const int32_t *tab = p.btable + ((int64_t)r * p.W + w) * p.brow_pages;
-    // The table's entries 32 tokens at a time, one per lane, as element
+    float qv[8];
+    qr.get(qv);
+    // The table's entries kL tokens at a time, one per lane, as element
     // offsets of the rows (-1: not there); then K and V rows four at a time.
-    for (int tb = 0; tb < n; tb += 32) {
-    int64_t where = -1;
-    if (tb + lane < n) {
-      const int pg = tab[(tb + lane) / p.bpage];
-      if (pg >= 0 && pg < p.bpages) where = (((int64_t)pg * p.Hkv + h) * p.bpage + (tb + lane) % p.bpage) * p.d;
-      else set_status(p.status, kStatusPage);
-    }
-    const int nb = min(32, n - tb);
-    for (int t0 = 4 * part; t0 < nb; t0 += 4 * kWpr) {
-      float s[4], kk[4][N], vv[4][N];
+    for (int tb = 0; tb < most; tb += kL) {
+      int64_t where = -1;
+      if (tb + gl < n) {
+        const int at = (tb + gl) / p.bpage, pg = tab[at];
+        if (pg >= 0 && pg < p.bpages) where = (((int64_t)pg * p.Hkv + h) * p.bpage + (tb + gl - at * p.bpage)) * p.d;
+        else set_status(p.status, kStatusPage);
+      }
+      const int nb = min(kL, most - tb);
+      for (int t0 = 4 * part; t0 < nb; t0 += 4 * kWpr) {
+        C kk[4], vv[4];
+        float s[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t at = __shfl_sync(0xffffffffu, where, t0 + j);
-        s[j] = at >= 0 ? 0.f : -CUDART_INF_F;
-        if (at >= 0) {
-          C::load(bk + at, lane, p.d, kk[j]);
-          C::load(bv + at, lane, p.d, vv[j]);
-        } else {
+        for (int j = 0; j < 4; ++j) {
+          const int64_t at = __shfl_sync(0xffffffffu, where, t0 + j, kL);
+          s[j] = at >= 0 ? 0.f : -CUDART_INF_F;
+          if (at >= 0) {
+            kk[j].load(bk + at, gl, p.d);
+            vv[j].load(bv + at, gl, p.d);
+          } else {
+            kk[j].zero();
+            vv[j].zero();
+          }
+        }
+        float top = mx;
 #pragma unroll
-          for (int i = 0; i < N; ++i) kk[j][i] = vv[j][i] = 0.f;
+        for (int j = 0; j < 4; ++j) {
+          float x[8];
+          kk[j].get(x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s[j] += qv[i] * x[i];
+          // A missing token's -inf stays -inf through the sum over lanes.
+          s[j] = group_sum(s[j]) * p.scale_log2;
+          top = fmaxf(top, s[j]);
+        }
+        const float f = exp2_sub(mx, top);
+        mx = top;
+        sum *= f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] *= f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float e = exp2_sub(s[j], mx);
+          float x[8];
+          vv[j].get(x);
+          sum += e;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[i] += e * x[i];
         }
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < N; ++i) s[j] += qv[i] * kk[j][i];
-      float top = mx;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        // A missing token's -inf stays -inf through the sum over lanes.
-        s[j] = warp_sum(s[j]) * p.scale_log2;
-        top = fmaxf(top, s[j]);
-      }
-      const float f = exp2_sub(mx, top);
-      mx = top;
-      sum *= f;
-#pragma unroll
-      for (int i = 0; i < N; ++i) acc[i] *= f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float e = exp2_sub(s[j], mx);
-        sum += e;
-#pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] += e * vv[j][i];
-      }
-    }
     }
   }
   ptx::pdl_wait();
-  if (live) {
-    for (int c0 = 0; c0 < pieces; c0 += 32 * kWpr) {
-      // One piece's (maximum, sum) per lane, then the outputs weighted by them.
-      const int mine = c0 + lane * kWpr + part;
-      float2 ml = make_float2(-CUDART_INF_F, 0.f);
-      if (mine < pieces) ml = p.part_ml[part_row(p, off + mine, h, m)];
-      const float mnew = fmaxf(mx, warp_max(ml.x));
-      const float f = exp2_sub(mx, mnew), e = exp2_sub(ml.x, mnew);
-      sum = sum * f + warp_sum(ml.y * e);
-      mx = mnew;
+  ptx::pdl_launch_dependents();
+  for (int c0 = 0; c0 < pieces; c0 += kL * kWpr) {
+    // One piece's (maximum, sum) per lane, then the outputs weighted by them.
+    const int mine = c0 + gl * kWpr + part;
+    float2 ml = make_float2(-CUDART_INF_F, 0.f);
+    if (mine < pieces) ml = p.part_ml[part_row(p, off + mine, h, m)];
+    float mnew = ml.x;
 #pragma unroll
-      for (int i = 0; i < N; ++i) acc[i] *= f;
-      const int n = (min(32 * kWpr, pieces - c0) - part + kWpr - 1) / kWpr;
+    for (int o = kL / 2; o; o >>= 1) mnew = fmaxf(mnew, __shfl_xor_sync(0xffffffffu, mnew, o));
+    mnew = fmaxf(mx, mnew);
+    const float f = exp2_sub(mx, mnew), e = exp2_sub(ml.x, mnew);
+    sum = sum * f + group_sum(ml.y * e);
+    mx = mnew;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] *= f;
+    const int n = (min(kL * kWpr, pieces - c0) - part + kWpr - 1) / kWpr;
 #pragma unroll 4
-      for (int j = 0; j < n; ++j) {
-        const float ej = __shfl_sync(0xffffffffu, e, j);
-        float x[N];
-        C::load(p.part_o + part_row(p, off + c0 + j * kWpr + part, h, m) * p.d, lane, p.d, x);
+    for (int j = 0; j < n; ++j) {
+      const float ej = __shfl_sync(0xffffffffu, e, j, kL);
+      Cols<float, kD> x;
+      x.load(p.part_o + part_row(p, off + c0 + j * kWpr + part, h, m) * p.d, gl, p.d);
+      float y[8];
+      x.get(y);
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] += ej * x[i];
-      }
+      for (int i = 0; i < 8; ++i) acc[i] += ej * y[i];
     }
   }
   if constexpr (kWpr > 1) {
     // Warps' results through shared memory, joined by the first.
-    if (lane == 0) wml[warp] = make_float2(mx, sum);
+    if (gl == 0) wml[warp][grp] = make_float2(mx, sum);
 #pragma unroll
-    for (int i = 0; i < N; ++i) wacc[warp][lane + 32 * i] = acc[i];
+    for (int i = 0; i < 8; ++i) wacc[warp][lane + 32 * i] = acc[i];
     __syncthreads();
     if (warp != 0) return;
     float top = -CUDART_INF_F;
 #pragma unroll
-    for (int j = 0; j < kWpr; ++j) top = fmaxf(top, wml[j].x);
+    for (int j = 0; j < kWpr; ++j) top = fmaxf(top, wml[j][grp].x);
     sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = 0.f;
+    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
 #pragma unroll
     for (int j = 0; j < kWpr; ++j) {
-      const float f = exp2_sub(wml[j].x, top);
-      sum += wml[j].y * f;
+      const float f = exp2_sub(wml[j][grp].x, top);
+      sum += wml[j][grp].y * f;
 #pragma unroll
-      for (int i = 0; i < N; ++i) acc[i] += wacc[j][lane + 32 * i] * f;
+      for (int i = 0; i < 8; ++i) acc[i] += wacc[j][lane + 32 * i] * f;
     }
     mx = top;
   }
-  if (!live) return;
+  if (want >= rows) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int64_t orow = ((int64_t)r * p.W + w) * p.Hq + hq;
 #pragma unroll
-  for (int i = 0; i < N; ++i) acc[i] *= inv;
-  C::store(static_cast<T *>(p.o) + orow * p.d, lane, p.d, acc);
-  if (lane == 0) {
+  for (int i = 0; i < 8; ++i) acc[i] *= inv;
+  C::store(static_cast<T *>(p.o) + orow * p.d, gl, p.d, acc);
+  if (gl == 0) {
     const float l2 = sum == 0.f ? -CUDART_INF_F : mx + log2f(sum);
     if (p.lse) p.lse[orow] = l2 * kLn2;
     if (p.lse2) p.lse2[((int64_t)r * p.Hkv + h) * p.M + m] = l2;
@@ -482,6 +539,7 @@ __global__ void __launch_bounds__(kThreads) attn_mass(AttnParams p) {
   const int rh = blockIdx.x / chunks, r = rh / p.Hkv;
   const int len = prompt_len(p, r);
   ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
   if (pos >= len) return;
   const float *l2 = p.lse2 + (int64_t)rh * p.M, *sc = p.scores + (int64_t)rh * p.M * p.cap + pos;
   float t[kP];
@@ -603,16 +661,17 @@ cudaError_t run_simt(const AttnParams &p, cudaStream_t s) {
     if (at % 4) f = attn_simt<T, 2, kRows>;
   const cudaError_t e = ensure_smem_limit((const void *)f, smem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(f, (unsigned)((long long)p.parts * p.Hkv * p.row_tiles), kThreads, smem, false, s, p);
+  return launch_kernel(f, (unsigned)((long long)p.parts * p.Hkv * p.row_tiles), kThreads, smem, true, s, p);
 }
 
 template <typename T, int kD>
 cudaError_t run_join_d(const AttnParams &p, cudaStream_t s) {
-  const int rows = p.W * p.Hq;
-  // Eight warps a row while that is at most about one wave of warps.
-  if ((long long)p.R * rows <= 8 * kAttnSMs)
-    return launch_kernel(attn_join<T, kD, 8>, (unsigned)(p.R * rows), 256, 0, true, s, p);
-  return launch_kernel(attn_join<T, kD, 1>, (unsigned)((long long)p.R * ((rows + 3) / 4)), 128, 0, true, s, p);
+  constexpr int kRpw = 32 / Cols<T, kD>::kLanes;  // rows a warp joins
+  const long long rows = (long long)p.W * p.Hq;
+  // Eight warps for a warp's rows while that is at most about one wave of warps.
+  if (p.R * rows <= 8LL * kRpw * kAttnSMs)
+    return launch_kernel(attn_join<T, kD, 8>, (unsigned)(p.R * ((rows + kRpw - 1) / kRpw)), 256, 0, true, s, p);
+  return launch_kernel(attn_join<T, kD, 1>, (unsigned)(p.R * ((rows + 4 * kRpw - 1) / (4 * kRpw))), 128, 0, true, s, p);
 }
 
 template <typename T>

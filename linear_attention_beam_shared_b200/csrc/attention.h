@@ -276,6 +276,11 @@ int attn_narrow_ctas(int d);                                           // CTAs o
 cudaError_t launch_attn_wide(const AttnParams &p, cudaStream_t s);    // attention_wide.cu
 cudaError_t launch_attn_mass_wide(const AttnParams &p, cudaStream_t s);
 
+// pdl: the kernel may be launched while the one before it in the stream still
+// runs (programmatic dependent launch).  Every kernel launched so waits for that one
+// before it touches anything the stream's earlier work may write, and lets its own
+// successor start only after that wait; so when a kernel runs, all but
+// its immediate predecessor are complete.
 template <typename... P, typename... A>
 cudaError_t launch_kernel(void (*f)(P...), unsigned grid, unsigned threads, size_t smem, bool pdl, cudaStream_t s, A... a) {
   cudaLaunchConfig_t cfg = {};

@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) attn_narrow(const __g
   __shared__ uint32_t live[kWarps][C::kStages];  // by warp and stage: the tile's tokens that are there
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h = blockIdx.x % p.Hkv;
+  ptx::pdl_wait();
   ptx::pdl_launch_dependents();
   PlanWalk walk;
   walk.begin<kThreads>(p, plan, blockIdx.x / p.Hkv);
@@ -349,7 +350,7 @@ cudaError_t run(const AttnParams &p, cudaStream_t s) {
   static_assert(kWarps * 8 * kNT * (D + 4) * 4 <= Cfg<D>::kSmem, "the warps' outputs go through the ring");
   const cudaError_t e = ensure_smem_limit((const void *)attn_narrow<D, kNT>, Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(attn_narrow<D, kNT>, (unsigned)(p.parts * p.Hkv), kThreads, Cfg<D>::kSmem, false, s, p);
+  return launch_kernel(attn_narrow<D, kNT>, (unsigned)(p.parts * p.Hkv), kThreads, Cfg<D>::kSmem, true, s, p);
 }
 
 }  // namespace

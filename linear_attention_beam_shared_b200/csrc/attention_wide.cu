@@ -128,11 +128,12 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
     ptx::tmem_alloc(&sh.tmem, kTmemCols);
     ptx::tmem_relinquish();
   }
-  ptx::pdl_launch_dependents();
-  PlanWalk walk;
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
+  PlanWalk walk;
   walk.begin<C::kThreads>(p, sh.plan, part);
   const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
   bool dead = false;
@@ -479,7 +480,10 @@ __global__ void __launch_bounds__(MassCfg<D>::kThreads, 1) attn_mass_wide(const 
   const int chunks = (p.cap + 127) / 128;
   const int t0 = (int)(blockIdx.x % chunks) * 128, rh = blockIdx.x / chunks, r = rh / p.Hkv, h = rh % p.Hkv;
   const int len = prompt_len(p, r);
-  if (t0 >= len) return;
+  if (t0 >= len) {
+    ptx::pdl_wait();  // a launch is never over before the one it depends on
+    return;
+  }
   const int nt = (p.M + 63) / 64;  // tiles of Q rows
 
   if (tid == 0) {
@@ -641,7 +645,7 @@ cudaError_t run(const AttnParams &p, cudaStream_t s) {
                    !encode_rows(&maps.v, p.v, D, 1, p.page, p.pages * p.Hkv, maps.box)))
     return cudaErrorInvalidValue;
   return launch_kernel(attn_wide<D, kSub>, (unsigned)((long long)p.parts * p.Hkv * p.row_tiles), C::kThreads, C::kSmem,
-                       false, s, p, maps);
+                       true, s, p, maps);
 }
 
 }  // namespace

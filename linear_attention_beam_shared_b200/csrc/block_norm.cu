@@ -13,7 +13,9 @@
 #include <algorithm>
 
 #include "../../include/onela.h"
+#include "attention.h"
 #include "internal.h"
+#include "sm100_ptx.h"
 
 namespace onela {
 namespace {
@@ -170,6 +172,8 @@ __global__ void __launch_bounds__(kMaxThreads, kV == 4 || (kV == 2 && !kLoop) ? 
   __shared__ __align__(16) float red[2][32];
   int sums = 0;
   const int tid = threadIdx.x, nt = blockDim.x, nv = p.D / 8, gv = p.group / 8;
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
   if (tid < 64) red[tid >> 5][tid & 31] = 0.f;
   const bool has_y = kAll || p.y, has_g = kAll || p.gate, has_x = kAll || p.x, has_post = kAll || p.w_post;
   const bool has_pre = kAll || p.w_pre, has_out = kAll || p.x_out, whole = kAll || p.group == p.D;
@@ -327,6 +331,8 @@ __global__ void __launch_bounds__(256) block_norm_any(BlockNormParams p) {
   int sums = 0;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row = blockIdx.x;
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
   if (tid < 64) red[tid >> 5][tid & 31] = 0.f;
   __syncthreads();
   float *inv = buf + p.D;
@@ -378,8 +384,7 @@ cudaError_t run_vec(const BlockNormParams &p, int threads, cudaStream_t s) {
   const int gv = p.group / 8;
   const bool sums = p.y && p.w_post && p.group != p.D && !(gv <= 32 && (gv & (gv - 1)) == 0);
   const size_t gs = sums ? (size_t)p.D / 8 * 4 : 0;
-  block_norm_vec<kYBf, kBf, kV, false, false, kMaxThreads><<<(unsigned)p.N, threads, gs, s>>>(p);
-  return cudaGetLastError();
+  return launch_kernel(block_norm_vec<kYBf, kBf, kV, false, false, kMaxThreads>, (unsigned)p.N, threads, gs, true, s, p);
 }
 
 // Rows looping over CTAs; false if there are too few rows for the CTAs that run at once.
@@ -394,10 +399,7 @@ bool run_loop(const BlockNormParams &p, int threads, cudaStream_t s, cudaError_t
   const bool all = p.y && p.gate && p.x && p.w_post && p.group == p.D && p.w_pre && p.x_out;
   auto f = all ? block_norm_vec<kYBf, kBf, kV, true, true> : block_norm_vec<kYBf, kBf, kV, true, false>;
   e = ensure_smem_limit((const void *)f, smem);
-  if (e == cudaSuccess) {
-    f<<<(unsigned)ctas, threads, smem, s>>>(p);
-    e = cudaGetLastError();
-  }
+  if (e == cudaSuccess) e = launch_kernel(f, (unsigned)ctas, threads, smem, true, s, p);
   return true;
 }
 
@@ -433,8 +435,7 @@ cudaError_t launch_block_norm(const BlockNormParams &p, cudaStream_t s) {
   const size_t smem = (size_t)(p.D + p.D / p.group) * 4;
   cudaError_t e = ensure_smem_limit((const void *)block_norm_any, smem);
   if (e != cudaSuccess) return e;
-  block_norm_any<<<(unsigned)p.N, 256, smem, s>>>(p);
-  return cudaGetLastError();
+  return launch_kernel(block_norm_any, (unsigned)p.N, 256, smem, true, s, p);
 }
 
 }  // namespace onela

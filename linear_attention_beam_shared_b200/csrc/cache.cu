@@ -10,6 +10,7 @@
 #include <algorithm>
 
 #include "../../include/onela.h"
+#include "attention.h"
 #include "cache.h"
 #include "internal.h"
 #include "sm100_ptx.h"
@@ -29,6 +30,8 @@ __device__ __forceinline__ void flag(int32_t *status, int32_t bit) {
 // row start allows; (token, head) rows are contiguous on both sides.
 template <typename U>
 __global__ void __launch_bounds__(256) cache_write(CacheWriteParams p) {
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
   const int per_row = p.row_bytes / (int)sizeof(U);  // units of a (token, head) row
   const int per_tok = per_row * p.Hkv;
   const int64_t i0 = (int64_t)blockIdx.x * 512, tok0 = i0 / per_tok;
@@ -138,6 +141,8 @@ template <bool kBig>
 __global__ void __launch_bounds__(kSel, 2) evict_select(CacheEvictParams p) {
   extern __shared__ __align__(16) uint32_t keys[];
   __shared__ EvictSel sm;
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
   cg::cluster_group cluster = cg::this_cluster();
   const int csize = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -151,7 +156,6 @@ __global__ void __launch_bounds__(kSel, 2) evict_select(CacheEvictParams p) {
     p.dst_lengths[r] = n;
     if (given != len) flag(p.status, ONELA_STATUS_LENGTH);
   }
-  ptx::pdl_launch_dependents();
   for (int e = rank * kSel + tid; e < rec; e += csize * kSel) kept[want + e] = free_len + e;
   for (int e = n + rank * kSel + tid; e < p.keep; e += csize * kSel) kept[e] = -1;
   if (want == free_len) {  // all of them stay
@@ -358,6 +362,7 @@ __global__ void __launch_bounds__(kSel, 2) evict_select(CacheEvictParams p) {
 template <int kLog>
 __global__ void __launch_bounds__(256) evict_copy_rows(CacheEvictParams p) {
   ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int groups = (p.keep + 7) / 8;
   const int64_t wid = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -410,6 +415,7 @@ __global__ void __launch_bounds__(256) evict_copy_rows(CacheEvictParams p) {
 template <typename U>
 __global__ void __launch_bounds__(256) evict_copy(CacheEvictParams p) {
   ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
   const int per_row = p.row_bytes / (int)sizeof(U);
   const int64_t per_rh = (int64_t)per_row * p.keep;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -439,19 +445,10 @@ __global__ void __launch_bounds__(256) evict_copy(CacheEvictParams p) {
   reinterpret_cast<U *>(p.dst_v)[dst] = vv;
 }
 
-template <typename F>
-cudaError_t launch_after(F *f, int64_t grid, const CacheEvictParams &p, cudaStream_t s) {
+template <typename F, typename P>
+cudaError_t launch_pdl(F *f, int64_t grid, const P &p, cudaStream_t s) {
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, f, p);
+  return launch_kernel(f, (unsigned)grid, 256, 0, true, s, p);
 }
 
 // The widest unit of 16, 8, 4 or 2 bytes that divides x.
@@ -469,12 +466,10 @@ cudaError_t launch_cache_write(const CacheWriteParams &p, cudaStream_t s) {
   const int u = unit_of(all);
   const int64_t units = (int64_t)p.row_bytes / u * p.Hkv * p.n * p.B;
   const int64_t grid = (units + 511) / 512;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  if (u == 16) cache_write<uint4><<<(unsigned)grid, 256, 0, s>>>(p);
-  else if (u == 8) cache_write<uint2><<<(unsigned)grid, 256, 0, s>>>(p);
-  else if (u == 4) cache_write<uint32_t><<<(unsigned)grid, 256, 0, s>>>(p);
-  else cache_write<uint16_t><<<(unsigned)grid, 256, 0, s>>>(p);
-  return cudaGetLastError();
+  if (u == 16) return launch_pdl(cache_write<uint4>, grid, p, s);
+  if (u == 8) return launch_pdl(cache_write<uint2>, grid, p, s);
+  if (u == 4) return launch_pdl(cache_write<uint32_t>, grid, p, s);
+  return launch_pdl(cache_write<uint16_t>, grid, p, s);
 }
 
 cudaError_t launch_cache_evict(const CacheEvictParams &p, cudaStream_t s) {
@@ -493,12 +488,14 @@ cudaError_t launch_cache_evict(const CacheEvictParams &p, cudaStream_t s) {
   cfg.blockDim = dim3(kSel);
   cfg.dynamicSmemBytes = big ? 0 : (size_t)stretch * 4;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = csize;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, big ? evict_select<true> : evict_select<false>, p);
   if (e != cudaSuccess) return e;
   const uint64_t all = addr(p.dst_k) | addr(p.dst_v) | addr(p.k_pool) | addr(p.v_pool) | (uint64_t)p.row_bytes;
@@ -506,17 +503,17 @@ cudaError_t launch_cache_evict(const CacheEvictParams &p, cudaStream_t s) {
   const int64_t rows = (int64_t)p.R * p.Hkv;
   if (u == 16 && per_row >= 4 && per_row <= 64 && (per_row & (per_row - 1)) == 0) {
     const int64_t grid = (rows * ((p.keep + 7) / 8) + 7) / 8;
-    if (per_row == 4) return launch_after(evict_copy_rows<2>, grid, p, s);
-    if (per_row == 8) return launch_after(evict_copy_rows<3>, grid, p, s);
-    if (per_row == 16) return launch_after(evict_copy_rows<4>, grid, p, s);
-    if (per_row == 32) return launch_after(evict_copy_rows<5>, grid, p, s);
-    return launch_after(evict_copy_rows<6>, grid, p, s);
+    if (per_row == 4) return launch_pdl(evict_copy_rows<2>, grid, p, s);
+    if (per_row == 8) return launch_pdl(evict_copy_rows<3>, grid, p, s);
+    if (per_row == 16) return launch_pdl(evict_copy_rows<4>, grid, p, s);
+    if (per_row == 32) return launch_pdl(evict_copy_rows<5>, grid, p, s);
+    return launch_pdl(evict_copy_rows<6>, grid, p, s);
   }
   const int64_t grid = (rows * per_row * p.keep + 255) / 256;
-  if (u == 16) return launch_after(evict_copy<uint4>, grid, p, s);
-  if (u == 8) return launch_after(evict_copy<uint2>, grid, p, s);
-  if (u == 4) return launch_after(evict_copy<uint32_t>, grid, p, s);
-  return launch_after(evict_copy<uint16_t>, grid, p, s);
+  if (u == 16) return launch_pdl(evict_copy<uint4>, grid, p, s);
+  if (u == 8) return launch_pdl(evict_copy<uint2>, grid, p, s);
+  if (u == 4) return launch_pdl(evict_copy<uint32_t>, grid, p, s);
+  return launch_pdl(evict_copy<uint16_t>, grid, p, s);
 }
 
 }  // namespace onela
