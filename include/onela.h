@@ -464,6 +464,8 @@ ONELA_API int onela_decode_step_noalloc(const onela_config *cfg, int32_t t, int3
  *     contents need not be kept or cleared between calls; calls that may run
  *     at the same time (other streams, two captured graphs) need scratch of
  *     their own.
+ *   - Outputs must not overlap inputs, or one another, except where a call
+ *     says so.
  *   - `status` is a DEVICE int32 or NULL.  A call ORs ONELA_STATUS_* bits
  *     into it for what its device-side data got wrong; the caller clears it.
  *     Nothing out of range is read or written either way.
@@ -495,16 +497,18 @@ enum {
  * The new token's own k and v must be in the cache before the call
  * (onela_cache_write).  A row with nothing to attend to gives o = 0 and
  * lse = -inf.  Cache slots past a length are not used, whatever they hold.
- *   R, W, H_q, H_kv   >= 1; W * H_q / H_kv <= 65536.
+ *   R, W, H_q, H_kv   >= 1; R, H_kv <= 65535, W * H_q / H_kv <= 65536, R * W *
+ *                     H_q < 2^28.
  *   d                 head width, 1 .. 256.
  *   dtype             ONELA_F32 or ONELA_BF16: of q, the pools and o.
  *                     Products are accumulated and the softmax is taken in
  *                     fp32 either way.
  *   kernel            ONELA_KERNEL_AUTO; ONELA_KERNEL_SIMT (any shape) or
  *                     ONELA_KERNEL_TC (bf16, d in {64, 128, 256}, pools and q
- *                     rows on 16-byte boundaries) to force one.
+ *                     rows on 16-byte boundaries, o on 4) to force one.
  *   page, pages, row_pages
- *                     the prompt pool and the entries of a table row.
+ *                     the prompt pool and the entries of a table row; a row
+ *                     holds page * row_pages <= 2^30 tokens.
  *   beam_page, beam_pages, beam_row_pages
  *                     the beams' pool; all 0: no beam segment.
  *   q_stride          elements between q's tokens (>= H_q * d): q may be a

@@ -571,10 +571,12 @@ __global__ void __launch_bounds__(kThreads) attn_mass(AttnParams p) {
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // The tensor-core kernels take bf16 with d in {64, 128, 256}; the pools' and
-// q's rows must lie on 16-byte boundaries (pointers not yet known: assumed).
+// q's rows must lie on 16-byte boundaries, o on 4 (pointers not yet known:
+// assumed).
 bool tc_fits(const onela_attention_config &c, const AttnParams &p) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v) | reinterpret_cast<uintptr_t>(p.q);
-  return c.dtype == ONELA_BF16 && (c.d == 64 || c.d == 128 || c.d == 256) && c.q_stride % 8 == 0 && (at & 15) == 0;
+  return c.dtype == ONELA_BF16 && (c.d == 64 || c.d == 128 || c.d == 256) && c.q_stride % 8 == 0 && (at & 15) == 0 &&
+         (reinterpret_cast<uintptr_t>(p.o) & 3) == 0;
 }
 
 AttnKind choose(const onela_attention_config &c, const AttnParams &p) {

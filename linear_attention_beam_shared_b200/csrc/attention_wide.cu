@@ -366,6 +366,12 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
     }
     cp_wait<0>();
     tell(it);
+    // Boxes of a piece that was given up may still be on their way: no CTA
+    // ends before its copies have landed.
+    for (uint32_t i = it < 2 * NS ? 0 : it - 2 * NS; i < it; ++i) {
+      const uint32_t turn = (i >> 1) / NS;
+      if (!ptx::mbar_wait(full_bar(i), turn & 1, kWaitNs)) dead = true;
+    }
   } else {
     // ----------------------------------------------------------- products
     // One warp issues the scores and one the outputs, so that the waits of
@@ -643,7 +649,7 @@ cudaError_t run(const AttnParams &p, cudaStream_t s) {
   if ((long long)p.pages * p.Hkv > 0x7fffffffLL) maps.box = 0;
   if (maps.box && (!encode_rows(&maps.k, p.k, D, 1, p.page, p.pages * p.Hkv, maps.box) ||
                    !encode_rows(&maps.v, p.v, D, 1, p.page, p.pages * p.Hkv, maps.box)))
-    return cudaErrorInvalidValue;
+    maps.box = 0;
   return launch_kernel(attn_wide<D, kSub>, (unsigned)((long long)p.parts * p.Hkv * p.row_tiles), C::kThreads, C::kSmem,
                        true, s, p, maps);
 }

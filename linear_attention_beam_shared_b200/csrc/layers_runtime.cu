@@ -104,7 +104,7 @@ int onela_paged_attention(const onela_attention_config *cfg, const void *q, cons
   if (beams ? (!beam_k || !beam_v || !beam_table || !beam_lengths)
             : (beam_k || beam_v || beam_table || beam_lengths))
     return ONELA_ERR_ARG;
-  if (mass && !mass_out) return ONELA_ERR_ARG;
+  if ((mass && !mass_out) || o == q) return ONELA_ERR_ARG;
   const size_t es = esize(c.dtype);
   for (const void *x : {q, k_pool, v_pool, beam_k, beam_v, (const void *)o})
     if (!aligned(x, es)) return ONELA_ERR_ARG;
@@ -137,7 +137,7 @@ int onela_paged_attention(const onela_attention_config *cfg, const void *q, cons
 int onela_cache_write(const onela_cache_write_config *cfg, const void *k, const void *v, void *k_pool, void *v_pool,
                       const int32_t *table, const int32_t *start, const int32_t *counts, int32_t *status,
                       onela_stream stream) {
-  if (!cfg || !k || !v || !k_pool || !v_pool || !table || !start) return ONELA_ERR_ARG;
+  if (!cfg || !k || !v || !k_pool || !v_pool || !table || !start || k_pool == v_pool) return ONELA_ERR_ARG;
   const onela_cache_write_config c = *cfg;
   const int64_t row = (int64_t)c.H_kv * c.d;
   if (c.B < 1 || c.n < 1 || c.H_kv < 1 || c.H_kv > 65535 || c.d < 1 || c.d > 256 || !valid_dtype(c.dtype) ||
@@ -185,7 +185,7 @@ int onela_cache_evict(const onela_cache_evict_config *cfg, const void *k_pool, c
   const onela_cache_evict_config c = *cfg;
   if (!valid_evict(c)) return ONELA_ERR_ARG;
   // Lengths and weights are read by every head while they are written.
-  if (dst_lengths == lengths || dst_mass == mass) return ONELA_ERR_ARG;
+  if (dst_lengths == lengths || dst_mass == mass || dst_k == dst_v) return ONELA_ERR_ARG;
   const size_t es = esize(c.dtype);
   for (const void *x : {k_pool, v_pool, (const void *)dst_k, (const void *)dst_v})
     if (!aligned(x, es)) return ONELA_ERR_ARG;
@@ -232,7 +232,7 @@ int onela_block_norm(const onela_block_norm_config *cfg, const void *y, const vo
       c.act > ONELA_ACT_SILU || !(c.eps >= 0.f))
     return ONELA_ERR_ARG;
   if (c.N == 0) return ONELA_OK;  // empty tensors have no address
-  if ((!y && !x) || (!y && (gate || w_post || scale)) || (!x_out && !n_out) || ((n_out != nullptr) != (w_pre != nullptr)))
+  if ((!y && !x) || (!y && (gate || w_post || scale)) || (!x_out && !n_out) || (x_out && x_out == n_out) || ((n_out != nullptr) != (w_pre != nullptr)))
     return ONELA_ERR_ARG;
   if ((gate != nullptr) != (c.act != ONELA_ACT_NONE)) return ONELA_ERR_ARG;
   if ((y && c.y_stride < c.D) || (gate && c.gate_stride < c.D) || (x && c.x_stride < c.D)) return ONELA_ERR_ARG;

@@ -16,7 +16,7 @@ def attention(L, **change):
 
 
 def call_attention(L, cfg, scratch_bytes=1 << 40, **change):
-    a = dict(q=P, k=P, v=P, table=P, lengths=P, bk=None, bv=None, bt=None, bl=None, mass=None, mass_out=None, o=P,
+    a = dict(q=3 * P, k=P, v=P, table=P, lengths=P, bk=None, bv=None, bt=None, bl=None, mass=None, mass_out=None, o=P,
              lse=None, scratch=P)
     a.update(change)
     return L._lib.lib.onela_paged_attention(ctypes.addressof(cfg), *a.values(), scratch_bytes, None, None)
@@ -35,7 +35,8 @@ def test_attention_refuses_bad_config(field, value):
 
 @pytest.mark.parametrize("change", [
     dict(q=None), dict(k=None), dict(v=None), dict(table=None), dict(lengths=None), dict(o=None), dict(scratch=None),
-    dict(scratch=P + 16), dict(q=P + 1), dict(lengths=P + 2), dict(mass=P), dict(bk=P), dict(bk=P, bv=P, bt=P, bl=P)])
+    dict(scratch=P + 16), dict(q=P + 1), dict(lengths=P + 2), dict(o=P + 1), dict(mass=P), dict(bk=P), dict(bk=P, bv=P, bt=P, bl=P),
+    dict(q=2 * P, o=2 * P)])
 def test_attention_refuses_bad_pointers(change):
     import linear_attention_beam_shared_b200 as L
     assert call_attention(L, attention(L), **change) == L.ONELA_ERR_ARG
@@ -70,18 +71,20 @@ def write_cfg(L, **change):
 def test_write_refuses_bad_config(field, value):
     import linear_attention_beam_shared_b200 as L
     cfg = write_cfg(L, **{field: value})
-    assert L._lib.lib.onela_cache_write(ctypes.addressof(cfg), *[P] * 6, None, None, None) == L.ONELA_ERR_ARG
+    assert L._lib.lib.onela_cache_write(ctypes.addressof(cfg), P, P, P, 2 * P, P, P, None, None, None) == L.ONELA_ERR_ARG
 
 
 def test_write_refuses_bad_pointers():
     import linear_attention_beam_shared_b200 as L
     cfg = write_cfg(L)
+    good = [P, P, P, 2 * P, P, P]
     for i in range(6):
         for bad in (None, P + 1):
-            a = [P] * 6
+            a = list(good)
             a[i] = bad
             assert L._lib.lib.onela_cache_write(ctypes.addressof(cfg), *a, None, None, None) == L.ONELA_ERR_ARG
-    assert L._lib.lib.onela_cache_write(None, *[P] * 6, None, None, None) == L.ONELA_ERR_ARG
+    assert L._lib.lib.onela_cache_write(None, *good, None, None, None) == L.ONELA_ERR_ARG
+    assert L._lib.lib.onela_cache_write(ctypes.addressof(cfg), *[P] * 6, None, None, None) == L.ONELA_ERR_ARG  # one pool
 
 
 def evict_cfg(L, **change):
@@ -92,7 +95,7 @@ def evict_cfg(L, **change):
 
 
 def call_evict(L, cfg, bytes_=1 << 40, **change):
-    a = dict(k=P, v=P, table=P, lengths=P, mass=P, dk=P, dv=P, dt=P, dl=2 * P, dm=2 * P, kept=None, scratch=P)
+    a = dict(k=P, v=P, table=P, lengths=P, mass=P, dk=P, dv=3 * P, dt=P, dl=2 * P, dm=2 * P, kept=None, scratch=P)
     a.update(change)
     return L._lib.lib.onela_cache_evict(ctypes.addressof(cfg), *a.values(), bytes_, None, None)
 
@@ -110,7 +113,7 @@ def test_evict_refuses_bad_config(field, value):
 
 @pytest.mark.parametrize("change", [
     {n: None} for n in ("k", "v", "table", "lengths", "mass", "dk", "dv", "dt", "dl", "dm", "scratch")] + [
-    dict(k=P + 1), dict(mass=P + 2), dict(scratch=P + 8), dict(dl=P), dict(dm=P)])
+    dict(k=P + 1), dict(mass=P + 2), dict(scratch=P + 8), dict(dl=P), dict(dm=P), dict(dv=P)])
 def test_evict_refuses_bad_pointers(change):
     import linear_attention_beam_shared_b200 as L
     assert call_evict(L, evict_cfg(L), **change) == L.ONELA_ERR_ARG
@@ -125,7 +128,7 @@ def norm_cfg(L, **change):
 
 
 def call_norm(L, cfg, **change):
-    a = dict(y=P, gate=P, x=P, w_post=P, scale=P, w_pre=P, x_out=2 * P, n_out=2 * P)
+    a = dict(y=P, gate=P, x=P, w_post=P, scale=P, w_pre=P, x_out=2 * P, n_out=3 * P)
     a.update(change)
     return L._lib.lib.onela_block_norm(ctypes.addressof(cfg), *a.values(), None)
 
@@ -141,7 +144,8 @@ def test_norm_refuses_bad_config(field, value):
 
 @pytest.mark.parametrize("change", [
     dict(y=None, x=None), dict(y=None), dict(x_out=None, n_out=None), dict(w_pre=None), dict(n_out=None),
-    dict(gate=None), dict(gate=P + 1), dict(w_post=P + 2), dict(y=P + 2)])
+    dict(gate=None), dict(gate=P + 1), dict(w_post=P + 2), dict(y=P + 2),
+    dict(n_out=3 * P, x_out=3 * P)])
 def test_norm_refuses_bad_pointers(change):
     import linear_attention_beam_shared_b200 as L
     assert call_norm(L, norm_cfg(L), **change) == L.ONELA_ERR_ARG

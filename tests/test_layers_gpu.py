@@ -218,6 +218,41 @@ def test_attention_many_requests():
     check_attention(rand_q(rng, 300, 1, 4, 64, "bf16"), Cache(rng, lengths, 2, 16, 64, "bf16"))
 
 
+@pytest.mark.parametrize("R,W,H_q,H_kv,d,dtype", [(700, 1, 4, 2, 64, "bf16"), (33, 20, 4, 4, 64, "bf16"),
+                                                  (500, 5, 8, 2, 128, "bf16"), (100, 1, 3, 1, 40, "f32")])
+def test_attention_batches_longer_than_a_warp(R, W, H_q, H_kv, d, dtype):
+    rng = np.random.default_rng(R)
+    lengths = rng.integers(0, 40, R)
+    lengths[R // 2] = 700
+    cache = Cache(rng, lengths.tolist(), H_kv, 16, d, dtype, row_pages=45)
+    check_attention(rand_q(rng, R, W, H_q, d, dtype), cache, dtype=dtype)
+
+
+def test_attention_output_on_any_boundary():
+    """o, q and the pools at addresses that rule the vector paths out."""
+    import linear_attention_beam_shared_b200 as L
+    rng = np.random.default_rng(15)
+
+    def shifted(t):
+        u = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")[1:].view(t.shape)
+        return u.copy_(t)
+
+    for W, lengths in ((1, [40, 7]), (1, [600, 7]), (24, [300, 0])):
+        cache = Cache(rng, lengths, 2, 16, 128, "bf16")
+        q = rand_q(rng, 2, W, 8, 128, "bf16")
+        k, v, table, n = cache.dev()
+        ref = L.onela_paged_attention(q, k, v, table, n)
+        got = [L.onela_paged_attention(q, k, v, table, n, out=shifted(q)),
+               L.onela_paged_attention(shifted(q), shifted(k), shifted(v), table, n)]
+        check_attention(q, cache)
+        # Two kernels' results: each off by at most 2^-8 of its row's sum p |v|
+        # (P's rounding; that sum is at most max |v|) and half a step of o;
+        # the fp32 sums' part (below 2^-12) fits in the 1 % on top.
+        vmax = cache.v[torch.isfinite(cache.v)].abs().max().double()
+        for o in got:
+            assert ((o.double() - ref.double()).abs() <= 1.01 * 2.0 ** -7 * (ref.double().abs() + vmax)).all()
+
+
 def test_attention_long_row_is_split():
     """A row long enough for many pieces, against torch in 64 bits on the device."""
     import linear_attention_beam_shared_b200 as L
