@@ -74,10 +74,12 @@ struct Shared {
   PlanSmem plan;
 };
 
-// K and V pools as {64 elements, 1, tokens of a page, (page, head)}.
+// K and V pools as {64 elements, 1, tokens of a page, (page, head)}; q as {64
+// elements, the G heads of a group, 64 / G tokens, request}: 64 query rows.
 struct Maps {
-  CUtensorMap k, v;
-  int box;  // tokens per box: 16, 8, or 0 (pages not a multiple of 8: no boxes)
+  CUtensorMap k, v, q;
+  int box;    // tokens per box of K and V: 16, 8, or 0 (pages not a multiple of 8: no boxes)
+  int q_box;  // q comes in boxes (G divides 64)
 };
 
 template <int N>
@@ -153,17 +155,29 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
       // own): Q may be replaced.
       ptx::bar_sync(1, C::kSoft);
       if (kSub == 2 || grp == 0) {
-        // A warp brings its 32 rows, 32 16-byte chunks at a time.
+        // By boxes of 64 rows, or a warp brings its 32 rows, 32 16-byte chunks at a time.
         uint8_t *qd = smem + (kSub == 2 ? grp * C::kQ : 0);
-        constexpr int kPer = D / 8;
-        const int64_t mine = m < p.M ? ((int64_t)r * p.W + m / p.G) * p.q_stride + (int64_t)(h * p.G + m % p.G) * D : -1;
-#pragma unroll 8
-        for (int e = 0; e < kPer; ++e) {
-          const int rl = (e * 32 + lane) / kPer, cc = (e * 32 + lane) % kPer, rw = (warp & 3) * 32 + rl;
-          const int64_t at = __shfl_sync(0xffffffffu, mine, rl);
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (at >= 0) x = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + at) + cc);
-          *reinterpret_cast<uint4 *>(qd + (cc >> 3) * 16384 + ptx::swz128(rw, cc & 7)) = x;
+        if (maps.q_box) {
+          if (warp == 4 * grp && lane == 0) {
+            ptx::fence_proxy_async();  // the rows that went out through this memory were written by plain stores
+            ptx::mbar_expect_tx(&sh.q, C::kQ);
+#pragma unroll
+            for (int a = 0; a < 2 * (D / 64); ++a)
+              ptx::tma_load_4d(qd + (a >> 1) * 16384 + (a & 1) * 8192, &maps.q, (a >> 1) * 64, h * p.G,
+                               (m1 + (a & 1) * 64) / p.G, r, &sh.q);
+          }
+        } else {
+          constexpr int kPer = D / 8;
+          const int64_t mine =
+              m < p.M ? ((int64_t)r * p.W + m / p.G) * p.q_stride + (int64_t)(h * p.G + m % p.G) * D : -1;
+#pragma unroll 4
+          for (int e = 0; e < kPer; ++e) {
+            const int rl = (e * 32 + lane) / kPer, cc = (e * 32 + lane) % kPer, rw = (warp & 3) * 32 + rl;
+            const int64_t at = __shfl_sync(0xffffffffu, mine, rl);
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (at >= 0) x = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + at) + cc);
+            *reinterpret_cast<uint4 *>(qd + (cc >> 3) * 16384 + ptx::swz128(rw, cc & 7)) = x;
+          }
         }
       }
       ptx::fence_proxy_async();
@@ -438,6 +452,7 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
     if (nq > 0) {
       if (ptx::elect_one()) ptx::mma_commit(&sh.done[is_s]);
       if (!ptx::mbar_wait(&sh.done[is_s], 0, kWaitNs)) dead = true;
+      if (is_s && !ptx::mbar_wait(&sh.q, (nq - 1) & 1, kWaitNs)) dead = true;  // Q's boxes have landed
     }
   }
   if (dead) set_status(p.status, ONELA_STATUS_TIMEOUT);
@@ -457,8 +472,8 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
 // per position).  Recomputing costs half of the attention's products; keeping
 // the scores would cost 4 bytes a row and token, more than K and V themselves
 // from 64 rows on at d = 64.  One CTA per (request, head, 128 tokens): K is an operand
-// held in shared memory, tiles of 64 rows of Q pass through a ring, two groups of four
-// warps take them in turn.
+// held in shared memory, tiles of 64 rows of Q pass through a ring, two groups
+// of four warps take them in turn; two CTAs per SM for d <= 128.
 template <int D>
 struct MassCfg {
   static constexpr int kStages = 4;
@@ -470,12 +485,13 @@ struct MassCfg {
 struct MassShared {
   uint64_t k, full[4], empty[4], s[4], sfree[4], done;
   uint32_t tmem;
-  float lse2[4][64];  // by Q stage
+  alignas(16) float lse2[4][64];  // by Q stage
   float sums[128];
 };
 
 template <int D>
-__global__ void __launch_bounds__(MassCfg<D>::kThreads, 1) attn_mass_wide(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(MassCfg<D>::kThreads, D == 256 ? 1 : 2) attn_mass_wide(const __grid_constant__ AttnParams p,
+                                                                                            const __grid_constant__ Maps maps) {
   using C = MassCfg<D>;
   constexpr int NS = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -523,13 +539,15 @@ __global__ void __launch_bounds__(MassCfg<D>::kThreads, 1) attn_mass_wide(const 
       const int b = grp * 2 + (c & 1), st = t % NS;
       wait_warp(&sh.s[b], (c >> 1) & 1, dead);
       ptx::tc_fence_after();
-      float x[2][32];
-      ptx::tmem_ld32(tmem + lanes + b * 64, x[0]);
-      ptx::tmem_ld32(tmem + lanes + b * 64 + 32, x[1]);
-      ptx::tmem_ld_wait();
       float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < 64; ++i) a[i & 3] += ex2(fmaf(x[i >> 5][i & 31], p.scale_log2, -sh.lse2[st][i]));
+      for (int e = 0; e < 2; ++e) {
+        float x[32];
+        ptx::tmem_ld32(tmem + lanes + b * 64 + e * 32, x);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) a[i & 3] += ex2(fmaf(x[i], p.scale_log2, -sh.lse2[st][e * 32 + i]));
+      }
       sum += (a[0] + a[1]) + (a[2] + a[3]);
       ptx::tc_fence_before();
       ptx::mbar_arrive(&sh.sfree[b]);
@@ -556,12 +574,25 @@ __global__ void __launch_bounds__(MassCfg<D>::kThreads, 1) attn_mass_wide(const 
         const int pg = p.table[(int64_t)r * p.row_pages + pos / p.page];
         if (pg >= 0 && pg < p.pages) mine = (((int64_t)pg * p.Hkv + h) * p.page + pos % p.page) * (D * 2);
       }
+      if (maps.box && __all_sync(0xffffffffu, mine >= 0)) {
+        // Boxes of 16 or 8 tokens; this warp's share of the bytes is expected by its first lane.
+        if (lane == 0) ptx::mbar_expect_tx(&sh.k, 32 * D * 2);
+        __syncwarp();
+        if (lane % maps.box == 0) {
+          const int ph = (int)(mine / (D * 2) / p.page), pl = (int)(mine / (D * 2) % p.page);
+#pragma unroll
+          for (int a = 0; a < D / 64; ++a)
+            ptx::tma_load_4d(smem + a * 16384 + (lw * 32 + lane) * 128, &maps.k, a * 64, 0, pl, ph, &sh.k);
+        }
+        __syncwarp();
+      } else {
 #pragma unroll 4
-      for (int e = 0; e < kPer; ++e) {
-        const int rl = (e * 32 + lane) / kPer, cc = (e * 32 + lane) % kPer;
-        const int64_t at = __shfl_sync(0xffffffffu, mine, rl);
-        ptx::cp_async16(smem + (cc >> 3) * 16384 + ptx::swz128(lw * 32 + rl, cc & 7),
-                        static_cast<const uint8_t *>(p.k) + (at < 0 ? 0 : at + cc * 16), at < 0 ? 0 : 16);
+        for (int e = 0; e < kPer; ++e) {
+          const int rl = (e * 32 + lane) / kPer, cc = (e * 32 + lane) % kPer;
+          const int64_t at = __shfl_sync(0xffffffffu, mine, rl);
+          ptx::cp_async16(smem + (cc >> 3) * 16384 + ptx::swz128(lw * 32 + rl, cc & 7),
+                          static_cast<const uint8_t *>(p.k) + (at < 0 ? 0 : at + cc * 16), at < 0 ? 0 : 16);
+        }
       }
       ptx::cp_async_commit();
     }
@@ -578,6 +609,14 @@ __global__ void __launch_bounds__(MassCfg<D>::kThreads, 1) attn_mass_wide(const 
       const int64_t mine = lane < 16 && m < p.M
                                ? (((int64_t)r * p.W + m / p.G) * p.q_stride + (int64_t)(h * p.G + m % p.G) * D) * 2
                                : -1;
+      if (maps.q_box) {
+        if (lt == 0) {
+          ptx::mbar_expect_tx(&sh.full[st], C::kTile);
+#pragma unroll
+          for (int a = 0; a < D / 64; ++a)
+            ptx::tma_load_4d(dst + a * 8192, &maps.q, a * 64, h * p.G, t * 64 / p.G, r, &sh.full[st]);
+        }
+      } else
 #pragma unroll 4
       for (int e = 0; e < kPer / 2; ++e) {
         const int rl = (e * 32 + lane) / kPer, cc = (e * 32 + lane) % kPer;
@@ -605,6 +644,10 @@ __global__ void __launch_bounds__(MassCfg<D>::kThreads, 1) attn_mass_wide(const 
     }
     cp_wait<0>();
     tell(nt - 1);
+    // No CTA ends before its boxes have landed.
+    if (!ptx::mbar_wait(&sh.k, 0, kWaitNs)) dead = true;
+    for (int t = max(0, nt - NS); t < nt; ++t)
+      if (!ptx::mbar_wait(&sh.full[t % NS], (t / NS) & 1, kWaitNs)) dead = true;
   } else {
     // ----------------------------------------------------------- products
     constexpr uint32_t id = ptx::idesc_bf16_f32(128, 64);
@@ -638,18 +681,25 @@ __global__ void __launch_bounds__(MassCfg<D>::kThreads, 1) attn_mass_wide(const 
   }
 }
 
-template <int D, int kSub>
-cudaError_t run(const AttnParams &p, cudaStream_t s) {
-  using C = Cfg<D, kSub>;
-  cudaError_t e = ensure_smem_limit((const void *)attn_wide<D, kSub>, C::kSmem);
-  if (e != cudaSuccess) return e;
+// The tensor maps of a call; boxes are left out where a shape rules them out.
+Maps make_maps(const AttnParams &p) {
   Maps maps = {};
   maps.box = p.page % 16 == 0 ? 16 : (p.page % 8 == 0 ? 8 : 0);
   // Coordinates are 32-bit.
   if ((long long)p.pages * p.Hkv > 0x7fffffffLL) maps.box = 0;
-  if (maps.box && (!encode_rows(&maps.k, p.k, D, 1, p.page, p.pages * p.Hkv, maps.box) ||
-                   !encode_rows(&maps.v, p.v, D, 1, p.page, p.pages * p.Hkv, maps.box)))
+  if (maps.box && (!encode_rows(&maps.k, p.k, p.d, 1, p.page, p.pages * p.Hkv, maps.box) ||
+                   !encode_rows(&maps.v, p.v, p.d, 1, p.page, p.pages * p.Hkv, maps.box)))
     maps.box = 0;
+  maps.q_box = 64 % p.G == 0 && encode_heads(&maps.q, p.q, p.d, p.Hq, p.W, p.R, p.q_stride, p.G, 64 / p.G);
+  return maps;
+}
+
+template <int D, int kSub>
+cudaError_t run(const AttnParams &p, cudaStream_t s) {
+  using C = Cfg<D, kSub>;
+  const cudaError_t e = ensure_smem_limit((const void *)attn_wide<D, kSub>, C::kSmem);
+  if (e != cudaSuccess) return e;
+  const Maps maps = make_maps(p);
   return launch_kernel(attn_wide<D, kSub>, (unsigned)((long long)p.parts * p.Hkv * p.row_tiles), C::kThreads, C::kSmem,
                        true, s, p, maps);
 }
@@ -668,7 +718,7 @@ static cudaError_t run_mass(const AttnParams &p, cudaStream_t s) {
   const cudaError_t e = ensure_smem_limit((const void *)attn_mass_wide<D>, MassCfg<D>::kSmem);
   if (e != cudaSuccess) return e;
   return launch_kernel(attn_mass_wide<D>, (unsigned)((long long)p.R * p.Hkv * ((p.cap + 127) / 128)),
-                       MassCfg<D>::kThreads, MassCfg<D>::kSmem, true, s, p);
+                       MassCfg<D>::kThreads, MassCfg<D>::kSmem, true, s, p, make_maps(p));
 }
 
 cudaError_t launch_attn_mass_wide(const AttnParams &p, cudaStream_t s) {

@@ -38,5 +38,10 @@ __device__ __forceinline__ float4 bf16x4(const uint8_t *p) { return bf16x4(*rein
 // swizzle (the K-major operand layout), zeros outside the tensor.  False when
 // the driver's encoder is unavailable or rejects the tensor.
 bool encode_rows(CUtensorMap *m, const void *base, int d, int H, int W, int R, int box_rows = 32);
+// The same over tokens `stride` elements apart: [R][W] tokens of [H][d], box
+// {64, box_heads, box_tokens, 1}, so that a box holds box_tokens * box_heads
+// rows, the heads of a token next to one another.
+bool encode_heads(CUtensorMap *m, const void *base, int d, int H, int W, int R, int64_t stride, int box_heads,
+                  int box_tokens);
 
 }  // namespace onela
