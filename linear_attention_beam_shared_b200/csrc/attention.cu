@@ -366,26 +366,30 @@ struct Cols<T, 0> {
 };
 
 // Joins a row's pieces and the beam's own tokens.  A query row takes a group
-// of lanes (8, 16 or 32 for d = 64, 128, 256: 16 bytes of bf16 a lane), so
-// that a warp reads a beam's K and V once for several heads of a group.  kWpr
-// warps share those rows: 1 when there are rows enough to fill the SMs, 8 when
-// a few rows have many pieces (64 rows of 18 pieces: half the time).  The
-// beams' own tokens are few (a decode horizon) and differ from beam to beam,
-// so their scores are formed here, four tokens at a time.
-template <typename T, int kD, int kWpr>
-__global__ void __launch_bounds__(kWpr == 1 ? 128 : kWpr * 32, kWpr == 1 ? 5 : 2)
+// of lanes (8, 16 or 32 for d = 64, 128, 256: 16 bytes of bf16 a lane), and a
+// group of lanes takes kGr rows of one beam and key-value head, so that their
+// K and V are read once (kGr = 4 or 2 where that leaves 12 warps for every SM:
+// with 8192 rows of 256 and 7 beam tokens one row each makes three waves of
+// CTAs, and the whole call 45.5 instead of 43.7 us).  kWpr warps share those rows: 1 when there are rows enough to fill
+// the SMs, 8 when a few rows have many pieces (64 rows of 18 pieces: half the
+// time).  The beams' own tokens are few (a decode horizon) and differ from
+// beam to beam, so their scores are formed here, four tokens at a time.
+template <typename T, int kD, int kWpr, int kGr>
+__global__ void __launch_bounds__(kWpr == 1 ? 128 : kWpr * 32, kWpr == 1 ? (kGr == 1 ? 5 : kGr == 2 ? 4 : 3) : 2)
     attn_join(const __grid_constant__ AttnParams p) {
   using C = Cols<T, kD>;
   constexpr int kBlock = kWpr == 1 ? 128 : kWpr * 32, kL = C::kLanes;
-  constexpr int kRpw = 32 / kL, kRowsPer = kRpw * (kWpr == 1 ? 4 : 1);
+  constexpr int kRpw = 32 / kL, kSetsPer = kRpw * (kWpr == 1 ? 4 : 1);  // sets of kGr rows, of a warp and of a CTA
+  static_assert(kWpr == 1 || kGr == 1, "warps share single rows");
   __shared__ PlanSmem plan;
   __shared__ float2 wml[kWpr][kRpw];
   __shared__ float wacc[kWpr == 1 ? 1 : kWpr][kWpr == 1 ? 1 : 256];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gl = lane % kL, grp = lane / kL;
   const int part = kWpr == 1 ? 0 : warp;
-  const int rows = p.W * p.Hq, blocks = (rows + kRowsPer - 1) / kRowsPer;
+  const int sets = p.W * p.Hq / kGr, blocks = (sets + kSetsPer - 1) / kSetsPer;
   const int r = blockIdx.x / blocks;
-  const int want = (blockIdx.x % blocks) * kRowsPer + (kWpr == 1 ? warp * kRpw : 0) + grp, row = min(want, rows - 1);
+  const int want = (blockIdx.x % blocks) * kSetsPer + (kWpr == 1 ? warp * kRpw : 0) + grp;
+  const int row = min(want, sets - 1) * kGr;  // the first of the set
   int off, pieces;
   plan_row<kBlock>(p, plan, r, off, pieces);
   off *= p.per_slot;
@@ -398,21 +402,26 @@ __global__ void __launch_bounds__(kWpr == 1 ? 128 : kWpr * 32, kWpr == 1 ? 5 : 2
     return x;
   };
 
-  float acc[8], mx = -CUDART_INF_F, sum = 0.f;
+  float acc[kGr][8], mx[kGr], sum[kGr];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+  for (int g = 0; g < kGr; ++g) {
+    mx[g] = -CUDART_INF_F;
+    sum[g] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[g][i] = 0.f;
+  }
   // The beam's own tokens first: nothing of them comes from the split kernel,
   // which may still be running.
   if (p.bk) {
     const T *bk = static_cast<const T *>(p.bk), *bv = static_cast<const T *>(p.bv);
-    C qr;
-    qr.load(static_cast<const T *>(p.q) + ((int64_t)r * p.W + w) * p.q_stride + (int64_t)hq * p.d, gl, p.d);
+    C qr[kGr];
+#pragma unroll
+    for (int g = 0; g < kGr; ++g)
+      qr[g].load(static_cast<const T *>(p.q) + ((int64_t)r * p.W + w) * p.q_stride + (int64_t)(hq + g) * p.d, gl, p.d);
     const int bcap = p.brow_pages * p.bpage, given = p.blengths[(int64_t)r * p.W + w];
     const int n = given < 0 ? 0 : (given > bcap ? bcap : given), most = __reduce_max_sync(0xffffffffu, n);
     if (n != given && gl == 0) set_status(p.status, kStatusLength);
     const int32_t *tab = p.btable + ((int64_t)r * p.W + w) * p.brow_pages;
-    float qv[8];
-    qr.get(qv);
     // The table's entries kL tokens at a time, one per lane, as element
     // offsets of the rows (-1: not there); then K and V rows four at a time.
     for (int tb = 0; tb < most; tb += kL) {
@@ -425,43 +434,47 @@ __global__ void __launch_bounds__(kWpr == 1 ? 128 : kWpr * 32, kWpr == 1 ? 5 : 2
       const int nb = min(kL, most - tb);
       for (int t0 = 4 * part; t0 < nb; t0 += 4 * kWpr) {
         C kk[4], vv[4];
-        float s[4];
+        uint32_t there = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int64_t at = __shfl_sync(0xffffffffu, where, t0 + j, kL);
-          s[j] = at >= 0 ? 0.f : -CUDART_INF_F;
           if (at >= 0) {
             kk[j].load(bk + at, gl, p.d);
             vv[j].load(bv + at, gl, p.d);
+            there |= 1u << j;
           } else {
             kk[j].zero();
             vv[j].zero();
           }
         }
-        float top = mx;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float x[8];
-          kk[j].get(x);
+        for (int g = 0; g < kGr; ++g) {
+          float s[4], qv[8], x[8];
+          qr[g].get(qv);
+          float top = mx[g];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) s[j] += qv[i] * x[i];
-          // A missing token's -inf stays -inf through the sum over lanes.
-          s[j] = group_sum(s[j]) * p.scale_log2;
-          top = fmaxf(top, s[j]);
-        }
-        const float f = exp2_sub(mx, top);
-        mx = top;
-        sum *= f;
+          for (int j = 0; j < 4; ++j) {
+            kk[j].get(x);
+            float t = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] *= f;
+            for (int i = 0; i < 8; ++i) t += qv[i] * x[i];
+            t = group_sum(t) * p.scale_log2;
+            s[j] = (there >> j) & 1 ? t : -CUDART_INF_F;
+            top = fmaxf(top, s[j]);
+          }
+          const float f = exp2_sub(mx[g], top);
+          mx[g] = top;
+          sum[g] *= f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float e = exp2_sub(s[j], mx);
-          float x[8];
-          vv[j].get(x);
-          sum += e;
+          for (int i = 0; i < 8; ++i) acc[g][i] *= f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) acc[i] += e * x[i];
+          for (int j = 0; j < 4; ++j) {
+            const float e = exp2_sub(s[j], top);
+            vv[j].get(x);
+            sum[g] += e;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[g][i] += e * x[i];
+          }
         }
       }
     }
@@ -471,61 +484,77 @@ __global__ void __launch_bounds__(kWpr == 1 ? 128 : kWpr * 32, kWpr == 1 ? 5 : 2
   for (int c0 = 0; c0 < pieces; c0 += kL * kWpr) {
     // One piece's (maximum, sum) per lane, then the outputs weighted by them.
     const int mine = c0 + gl * kWpr + part;
-    float2 ml = make_float2(-CUDART_INF_F, 0.f);
-    if (mine < pieces) ml = p.part_ml[part_row(p, off + mine, h, m)];
-    float mnew = ml.x;
+    float2 ml[kGr];
 #pragma unroll
-    for (int o = kL / 2; o; o >>= 1) mnew = fmaxf(mnew, __shfl_xor_sync(0xffffffffu, mnew, o));
-    mnew = fmaxf(mx, mnew);
-    const float f = exp2_sub(mx, mnew), e = exp2_sub(ml.x, mnew);
-    sum = sum * f + group_sum(ml.y * e);
-    mx = mnew;
+    for (int g = 0; g < kGr; ++g) {
+      ml[g] = make_float2(-CUDART_INF_F, 0.f);
+      if (mine < pieces) ml[g] = p.part_ml[part_row(p, off + mine, h, m + g)];
+    }
+    float e[kGr];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] *= f;
+    for (int g = 0; g < kGr; ++g) {
+      float mnew = ml[g].x;
+#pragma unroll
+      for (int o = kL / 2; o; o >>= 1) mnew = fmaxf(mnew, __shfl_xor_sync(0xffffffffu, mnew, o));
+      mnew = fmaxf(mx[g], mnew);
+      const float f = exp2_sub(mx[g], mnew);
+      e[g] = exp2_sub(ml[g].x, mnew);
+      sum[g] = sum[g] * f + group_sum(ml[g].y * e[g]);
+      mx[g] = mnew;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[g][i] *= f;
+    }
     const int n = (min(kL * kWpr, pieces - c0) - part + kWpr - 1) / kWpr;
-#pragma unroll 4
+#pragma unroll(4 / kGr)
     for (int j = 0; j < n; ++j) {
-      const float ej = __shfl_sync(0xffffffffu, e, j, kL);
-      Cols<float, kD> x;
-      x.load(p.part_o + part_row(p, off + c0 + j * kWpr + part, h, m) * p.d, gl, p.d);
-      float y[8];
-      x.get(y);
+      Cols<float, kD> x[kGr];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += ej * y[i];
+      for (int g = 0; g < kGr; ++g) x[g].load(p.part_o + part_row(p, off + c0 + j * kWpr + part, h, m + g) * p.d, gl, p.d);
+#pragma unroll
+      for (int g = 0; g < kGr; ++g) {
+        const float ej = __shfl_sync(0xffffffffu, e[g], j, kL);
+        float y[8];
+        x[g].get(y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[g][i] += ej * y[i];
+      }
     }
   }
   if constexpr (kWpr > 1) {
     // Warps' results through shared memory, joined by the first.
-    if (gl == 0) wml[warp][grp] = make_float2(mx, sum);
+    if (gl == 0) wml[warp][grp] = make_float2(mx[0], sum[0]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) wacc[warp][lane + 32 * i] = acc[i];
+    for (int i = 0; i < 8; ++i) wacc[warp][lane + 32 * i] = acc[0][i];
     __syncthreads();
     if (warp != 0) return;
     float top = -CUDART_INF_F;
 #pragma unroll
     for (int j = 0; j < kWpr; ++j) top = fmaxf(top, wml[j][grp].x);
-    sum = 0.f;
+    sum[0] = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+    for (int i = 0; i < 8; ++i) acc[0][i] = 0.f;
 #pragma unroll
     for (int j = 0; j < kWpr; ++j) {
       const float f = exp2_sub(wml[j][grp].x, top);
-      sum += wml[j][grp].y * f;
+      sum[0] += wml[j][grp].y * f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += wacc[j][lane + 32 * i] * f;
+      for (int i = 0; i < 8; ++i) acc[0][i] += wacc[j][lane + 32 * i] * f;
     }
-    mx = top;
+    mx[0] = top;
   }
-  if (want >= rows) return;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int64_t orow = ((int64_t)r * p.W + w) * p.Hq + hq;
+  if (want >= sets) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] *= inv;
-  C::store(static_cast<T *>(p.o) + orow * p.d, gl, p.d, acc);
-  if (gl == 0) {
-    const float l2 = sum == 0.f ? -CUDART_INF_F : mx + log2f(sum);
-    if (p.lse) p.lse[orow] = l2 * kLn2;
-    if (p.lse2) p.lse2[((int64_t)r * p.Hkv + h) * p.M + m] = l2;
+  for (int g = 0; g < kGr; ++g) {
+    const float inv = sum[g] == 0.f ? 0.f : 1.f / sum[g];
+    const int64_t orow = ((int64_t)r * p.W + w) * p.Hq + hq + g;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[g][i] *= inv;
+    C::store(static_cast<T *>(p.o) + orow * p.d, gl, p.d, acc[g]);
+    if (gl == 0) {
+      const float l2 = sum[g] == 0.f ? -CUDART_INF_F : mx[g] + log2f(sum[g]);
+      if (p.lse) p.lse[orow] = l2 * kLn2;
+      if (p.lse2) p.lse2[((int64_t)r * p.Hkv + h) * p.M + m + g] = l2;
+    }
   }
 }
 
@@ -670,10 +699,16 @@ template <typename T, int kD>
 cudaError_t run_join_d(const AttnParams &p, cudaStream_t s) {
   constexpr int kRpw = 32 / Cols<T, kD>::kLanes;  // rows a warp joins
   const long long rows = (long long)p.W * p.Hq;
+  auto grid = [&](int per) { return (unsigned)(p.R * ((rows + per - 1) / per)); };
   // Eight warps for a warp's rows while that is at most about one wave of warps.
   if (p.R * rows <= 8LL * kRpw * kAttnSMs)
-    return launch_kernel(attn_join<T, kD, 8>, (unsigned)(p.R * ((rows + kRpw - 1) / kRpw)), 256, 0, true, s, p);
-  return launch_kernel(attn_join<T, kD, 1>, (unsigned)(p.R * ((rows + 4 * kRpw - 1) / (4 * kRpw))), 128, 0, true, s, p);
+    return launch_kernel(attn_join<T, kD, 8, 1>, grid(kRpw), 256, 0, true, s, p);
+  if constexpr (kD != 0) {
+    const long long most = p.R * rows / (12LL * kRpw * kAttnSMs);  // rows a set, 12 warps left for every SM
+    if (p.G % 4 == 0 && most >= 4) return launch_kernel(attn_join<T, kD, 1, 4>, grid(16 * kRpw), 128, 0, true, s, p);
+    if (p.G % 2 == 0 && most >= 2) return launch_kernel(attn_join<T, kD, 1, 2>, grid(8 * kRpw), 128, 0, true, s, p);
+  }
+  return launch_kernel(attn_join<T, kD, 1, 1>, grid(4 * kRpw), 128, 0, true, s, p);
 }
 
 template <typename T>
