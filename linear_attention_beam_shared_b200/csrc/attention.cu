@@ -125,19 +125,25 @@ __global__ void __launch_bounds__(kThreads, 4) attn_simt(AttnParams p) {
     const int r = walk.r, lo = walk.lo, hi = walk.hi, n = (hi - lo + kToks - 1) / kToks;
     __syncthreads();  // the previous piece's shared memory is read
     if (p.direct && h == 0 && rt == 0 && tid == 0 && p.lengths[r] != hi) set_status(p.status, kStatusLength);
-    // Element offset of this lane's token of step i (lanes 0 .. 7: the warp's 8 tokens); -1 if it is not there.
-    auto find = [&](int i) -> int64_t {
+    // The page and the place on it of this lane's token of step i (lanes 0 ..
+    // 7: the warp's 8 tokens).  The entry is looked at a step later, so that
+    // no warp waits for the table.
+    int pg = 0, place = 0;
+    auto look = [&](int i) {
       const int pos = lo + i * kToks + warp * 8 + lane;
-      if (lane >= 8 || pos >= hi) return -1;
-      const int pg = p.table[(int64_t)r * p.row_pages + pos / p.page];
-      if (pg < 0 || pg >= p.pages) {
-        set_status(p.status, kStatusPage);
-        return -1;
+      if (lane < 8 && pos < hi) {
+        const int at = pos / p.page;
+        pg = p.table[(int64_t)r * p.row_pages + at];
+        place = pos - at * p.page;
       }
-      return (((int64_t)pg * p.Hkv + h) * p.page + pos % p.page) * p.d;
     };
-    auto fill = [&](int i, int64_t row) {
+    auto fill = [&](int i) {
       if (i < n) {
+        int64_t row = -1;  // element offset of the token's row; -1 if it is not there
+        if (lane < 8 && lo + i * kToks + warp * 8 + lane < hi) {
+          if (pg >= 0 && pg < p.pages) row = (((int64_t)pg * p.Hkv + h) * p.page + place) * p.d;
+          else set_status(p.status, kStatusPage);
+        }
         const int st = i % L.stages;
         uint8_t *kd = ring + st * L.stage, *vd = kd + kToks * L.k_stride;
         const uint32_t bits = __ballot_sync(0xffffffffu, row >= 0);
@@ -169,10 +175,10 @@ __global__ void __launch_bounds__(kThreads, 4) attn_simt(AttnParams p) {
       }
       ptx::cp_async_commit();
     };
-    int64_t row = find(0);
+    look(0);
     for (int i = 0; i < L.stages - 1; ++i) {
-      fill(i, row);
-      row = find(i + 1);
+      fill(i);
+      look(i + 1);
     }
     for (int i = warp; i < kRows; i += 4) {
       const int m = m0 + i;
@@ -195,8 +201,8 @@ __global__ void __launch_bounds__(kThreads, 4) attn_simt(AttnParams p) {
       if (L.stages == 3) ptx::cp_async_wait_group1();
       else ptx::cp_async_wait_all();
       __syncthreads();  // step i is there for every warp, step i - 1 read by all
-      fill(i + L.stages - 1, row);
-      row = find(i + L.stages);
+      fill(i + L.stages - 1);
+      look(i + L.stages);
       const int st = i % L.stages;
       const uint8_t *ks = ring + st * L.stage, *vs = ks + kToks * L.k_stride;
       const uint32_t live = *reinterpret_cast<const uint32_t *>(there[st]);

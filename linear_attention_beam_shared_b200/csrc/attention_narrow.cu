@@ -98,22 +98,27 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) attn_narrow(const __g
     const int first = lo + warp * kTok;
     const int n = first < hi ? (hi - first + 63) / 64 : 0;
 
-    // Byte offset of a token's (token, head) row in the pools, -1 if it is
-    // not there: of this lane's token of tile i, or of the tile's first when
-    // it lies on one page.
-    auto row_of = [&](int i) -> int64_t {
+    // The page and the place on it of this lane's token of tile i, or of the
+    // tile's first when it lies on one page.  The entry is looked at a tile
+    // later, so that no warp waits for the table.
+    int pg = 0, place = 0;
+    auto look = [&](int i) {
       const int pos = first + 64 * i + (one_page ? 0 : lane & 15);
-      if (i >= n || pos >= hi) return -1;
-      const int at = pos / p.page, pg = tab[at];
-      if (pg < 0 || pg >= p.pages) {
-        set_status(p.status, kStatusPage);
-        return -1;
+      if (i < n && pos < hi) {
+        const int at = pos / p.page;
+        pg = tab[at];
+        place = pos - at * p.page;
       }
-      return (((int64_t)pg * p.Hkv + h) * p.page + (pos - at * p.page)) * C::kRow;
     };
     // Copies of tile i into stage st: zeros for tokens that are not there.
-    auto issue = [&](int i, int st, int64_t row) {
+    auto issue = [&](int i, int st) {
       if (i < n) {
+        // Byte offset of the (token, head) row in the pools, -1 if it is not there.
+        int64_t row = -1;
+        if (first + 64 * i + (one_page ? 0 : lane & 15) < hi) {
+          if (pg >= 0 && pg < p.pages) row = (((int64_t)pg * p.Hkv + h) * p.page + place) * C::kRow;
+          else set_status(p.status, kStatusPage);
+        }
         uint8_t *kd = ring + st * 2 * C::kTile, *vd = kd + C::kTile;
         const int left = hi - (first + 64 * i);
         if (one_page) {
@@ -146,11 +151,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) attn_narrow(const __g
       ptx::cp_async_commit();
     };
 
-    int64_t row = row_of(0);
+    look(0);
 #pragma unroll 1
     for (int i = 0; i < C::kStages - 1; ++i) {
-      issue(i, i, row);
-      row = row_of(i + 1);
+      issue(i, i);
+      look(i + 1);
     }
 
     // Q^T as the B operand (column = query row g + 8 nt), rows past M zero.
@@ -185,8 +190,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) attn_narrow(const __g
       __syncwarp();
       {  // The stage read in the last round takes tile i + kStages - 1.
         const int fs = st == 0 ? C::kStages - 1 : st - 1;
-        issue(i + C::kStages - 1, fs, row);
-        row = row_of(i + C::kStages);
+        issue(i + C::kStages - 1, fs);
+        look(i + C::kStages);
       }
       const uint32_t k_u32 = ring_u32 + st * 2 * C::kTile, v_u32 = k_u32 + C::kTile;
       const uint32_t here = live[warp][st];
