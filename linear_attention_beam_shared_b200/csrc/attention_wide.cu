@@ -296,6 +296,7 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
     constexpr int kTokW = TT / 4;     // tokens of a tile this warp brings
     constexpr int kPer = D * 2 / 16;  // 16-byte chunks of a row
     const uint8_t *kp = static_cast<const uint8_t *>(p.k), *vp = static_cast<const uint8_t *>(p.v);
+    const bool one_page = p.page % 16 == 0;
     uint32_t it = 0;             // items (K and V tiles in turn) issued
     uint32_t told = 0, pend = 0;  // items reported full, and which of the others are for this warp to report
     auto full_bar = [&](uint32_t i) { return (i & 1) ? &sh.vfull[(i >> 1) % NS] : &sh.kfull[(i >> 1) % NS]; };
@@ -314,23 +315,34 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
     while (walk.next(p)) {
       const int32_t *tab = p.table + (int64_t)walk.r * p.row_pages;
       const int nt = (walk.hi - walk.lo + TT - 1) / TT;
-      // This lane's token of tile t: page * Hkv + head and the token's place in the page; -1 if it is not there.
-      int ph, place;
-      auto find = [&](int t) {
-        const int pos = walk.lo + t * TT + lw * kTokW + lane;
+      // Where this warp's 16 tokens of a tile are: page * Hkv + head (-1: not
+      // there) and place on the page, by lane.  Pages of a multiple of 16
+      // tokens hold them together: one entry for a tile, and the entries of 32
+      // tiles in one load.  Otherwise each lane looks its token's entry up a tile ahead.
+      int ph = -1, place = 0;
+      auto entry = [&](int pos) {
         ph = -1;
-        if (lane >= kTokW || t >= nt || pos >= walk.hi) return;
-        const int pg = tab[pos / p.page];
-        place = pos % p.page;
-        if (pg < 0 || pg >= p.pages) set_status(p.status, kStatusPage);
-        else ph = pg * p.Hkv + h;
+        if (pos < walk.hi) {
+          const int at = pos / p.page, pg = tab[at];
+          place = pos - at * p.page;
+          if (pg >= 0 && pg < p.pages) ph = pg * p.Hkv + h;
+          else set_status(p.status, kStatusPage);
+        }
       };
-      find(0);
+      const int first = walk.lo + lw * kTokW;
+      if (!one_page) entry(lane < kTokW ? first + lane : walk.hi);
       for (int t = 0; t < nt; ++t) {
-        const int cph = ph, cplace = place;
+        int cph = ph, cplace = place;
+        if (one_page) {
+          if (t % 32 == 0) entry(first + (t + lane) * TT);
+          cph = __shfl_sync(0xffffffffu, ph, t % 32);
+          cplace = __shfl_sync(0xffffffffu, place, t % 32) + lane;
+          if (lane >= kTokW || first + t * TT + lane >= walk.hi) cph = -1;
+        } else {
+          entry(lane < kTokW ? first + (t + 1) * TT + lane : walk.hi);
+        }
         const uint32_t here = __ballot_sync(0xffffffffu, cph >= 0);
         const bool boxes = maps.box && here == (1u << kTokW) - 1u;
-        find(t + 1);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv, ++it) {
           const uint32_t st = (it >> 1) % NS, n = (it >> 1) / NS;  // stage, and its uses before
