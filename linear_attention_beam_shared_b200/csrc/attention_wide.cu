@@ -130,6 +130,11 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
     ptx::tmem_alloc(&sh.tmem, kTmemCols);
     ptx::tmem_relinquish();
   }
+  if (tid == 32 && maps.box) {
+    ptx::prefetch_tmap(&maps.k);
+    ptx::prefetch_tmap(&maps.v);
+  }
+  if (tid == 64 && maps.q_box) ptx::prefetch_tmap(&maps.q);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
