@@ -11,6 +11,10 @@ The work runs in the CUDA library ``libonela_b200.so`` (C ABI in
 ``include/onela.h``); this package is its Python binding.  ``onela_*``
 functions mirror the C entry points one to one; ``BeamDecoder`` is a small
 convenience wrapper around a handle.
+
+Models with GDN layers interleave them with full-attention layers and norms.
+``onela_cache_write``, ``onela_paged_attention``, ``onela_cache_evict`` and
+``onela_block_norm`` are the operators between two GDN steps of such a model.
 """
 from __future__ import annotations
 
