@@ -618,3 +618,101 @@ def test_hybrid_decode():
         run_evict(cache, mass.cpu().numpy(), 40, 8, H, page, d, "bf16")
     finally:
         dec.close()
+
+
+def test_evict_within_one_pool_and_attend_again():
+    """The destination pages may lie in the source's pool; the cut cache is
+    then read like any other, and what was not moved is untouched."""
+    import linear_attention_beam_shared_b200 as L
+    rng = np.random.default_rng(20)
+    R, H, page, d, keep = 2, 2, 16, 128, 40
+    cache = Cache(rng, [150, 30], H, page, d, "bf16", row_pages=11, spare=10)
+    k, v, table, lengths = cache.dev()
+    free = np.setdiff1d(np.arange(k.shape[0]), cache.table).astype(np.int32)
+    new = torch.from_numpy(free[:R * 3].reshape(R, 3)).cuda()
+    mass = rng.random((R, H, 11 * page)).astype(np.float32)
+    before_k, before_v = f64(k), f64(v)
+    dl, dm = torch.zeros(R, dtype=torch.int32, device="cuda"), torch.zeros(R, H, 48, device="cuda")
+    L.onela_cache_evict(k, v, table, lengths, torch.from_numpy(mass).cuda(), keep, 5, k, v, new, dl, dm)
+    rk, rv, rm, rn, kept = layers.cache_evict(before_k, before_v, cache.table, cache.lengths, mass, keep, 5, before_k,
+                                              before_v, new.cpu().numpy(), np.zeros((R, H, 48)))
+    np.testing.assert_array_equal(f64(k), rk)
+    np.testing.assert_array_equal(f64(v), rv)
+    np.testing.assert_array_equal(dl.cpu().numpy(), rn)
+    cut = Cache.__new__(Cache)
+    cut.k, cut.v, cut.table, cut.lengths, cut.row_pages = k, v, new.cpu().numpy(), rn, 3
+    check_attention(rand_q(rng, R, 1, 4, d, "bf16"), cut)
+    # Per head: the same as attention over the kept tokens of the old cache.
+    assert (kept[0, 0] != kept[0, 1]).any()
+
+
+def test_two_streams_and_two_graphs_at_once():
+    """Calls of their own scratch on two streams, and two captured graphs
+    replayed at once, give what they give alone."""
+    import linear_attention_beam_shared_b200 as L
+    rng = np.random.default_rng(21)
+    jobs = []
+    for W in (1, 40):
+        cache = Cache(rng, [3000, 700], 2, 16, 128, "bf16")
+        k, v, table, lengths = cache.dev()
+        q = rand_q(rng, 2, W, 8, 128, "bf16")
+        m = torch.zeros(2, 2, cache.row_pages * 16, device="cuda")
+        jobs.append((q, k, v, table, lengths, m))
+
+    def call(j, s=None):
+        q, k, v, table, lengths, m = j
+        return L.onela_paged_attention(q, k, v, table, lengths, mass_out=m, stream=s)
+
+    ref = [(call(j).clone(), j[5].clone()) for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    outs = [[] for _ in jobs]
+    for _ in range(5):
+        for i, (j, s) in enumerate(zip(jobs, streams)):
+            outs[i].append(call(j, s))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, ref[i][0]) for o in outs[i]) and torch.equal(jobs[i][5], ref[i][1])
+    graphs = []
+    for j in jobs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            o = call(j)
+        graphs.append((g, o))
+    for _ in range(5):
+        for (g, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(graphs[i][1], ref[i][0]) and torch.equal(jobs[i][5], ref[i][1])
+
+
+@pytest.mark.parametrize("G,W", [(1, 40), (3, 20), (64, 1), (96, 1), (32, 5), (5, 60)])
+def test_attention_group_sizes(G, W):
+    """Grouped heads that do and do not divide a box of 64 query rows."""
+    rng = np.random.default_rng(G)
+    blen = rng.integers(0, 4, (2, W))
+    blen[0, 0] = 3
+    cache = Cache(rng, [130, 64], 2, 16, 64, "bf16")
+    check_attention(rand_q(rng, 2, W, 2 * G, 64, "bf16"), cache, beam=draw_beam(rng, 2, W, 2, 64, "bf16", blen),
+                    mass=rng.random((2, 2, cache.row_pages * 16)).astype(np.float32))
+
+
+def test_attention_other_requests_nan_stays_theirs():
+    """NaN in one request's query and cache leaves the others' rows alone."""
+    import linear_attention_beam_shared_b200 as L
+    rng = np.random.default_rng(22)
+    for W in (1, 20, 70):
+        cache = Cache(rng, [200, 90, 100], 2, 16, 64, "bf16")
+        q = rand_q(rng, 3, W, 8, 64, "bf16")
+        k, v, table, lengths = cache.dev()
+        m = torch.zeros(3, 2, cache.row_pages * 16, device="cuda")
+        ref = L.onela_paged_attention(q, k, v, table, lengths, mass_out=m).clone()
+        rm = m.clone()
+        q[1] = float("nan")
+        k[table[1, 0].long()] = float("nan")
+        o = L.onela_paged_attention(q, k, v, table, lengths, mass_out=m)
+        assert torch.isnan(o[1].float()).all()
+        for r in (0, 2):
+            assert torch.equal(o[r], ref[r]) and torch.equal(m[r], rm[r])
