@@ -513,7 +513,7 @@ enum {
  *                     the beams' pool; all 0: no beam segment.
  *   q_stride          elements between q's tokens (>= H_q * d): q may be a
  *                     slice of a wider projection.
- *   scale             > 0. */
+ *   scale             > 0, at most 2e38. */
 typedef struct {
   int32_t R, W, H_q, H_kv, d;
   int32_t dtype;
@@ -541,7 +541,10 @@ typedef struct {
  *   o            [R][W][H_q][d] in dtype, written.
  *   lse          fp32 [R][W][H_q] or NULL: log sum_j exp(s_j).
  *   scratch      at least onela_paged_attention_scratch_bytes(cfg, want_mass)
- *                bytes (want_mass: whether mass_out is given); 0 for a bad cfg.
+ *                bytes (want_mass: whether mass_out is given); 0 for a bad
+ *                cfg, or when none is needed.  With ONELA_KERNEL_AUTO a call
+ *                whose pointers rule the tensor-core kernel out takes the
+ *                other one, which needs the bytes of ONELA_KERNEL_SIMT.
  * Errors: ONELA_ERR_ARG, ONELA_ERR_SCRATCH, ONELA_ERR_UNSUPPORTED (the forced
  * kernel cannot run this shape), ONELA_ERR_CUDA. */
 ONELA_API size_t onela_paged_attention_scratch_bytes(const onela_attention_config *cfg, int32_t want_mass);

@@ -6,6 +6,8 @@ these once per layer and step, so the sizes of a call (its configuration
 struct and scratch size, plain numbers) are remembered by their values.
 Nothing else is kept between calls.
 
+They take no part in autograd: their outputs carry no gradient.
+
 ``stream``: None for the current stream of the tensors' device, a
 ``torch.cuda.Stream`` or a raw stream number.  What a call allocates (outputs
 not given, scratch) is allocated on that stream.
@@ -17,7 +19,7 @@ import math
 
 import torch
 
-from ._lib import ONELA_KERNEL_AUTO, _check, lib
+from ._lib import ONELA_KERNEL_AUTO, ONELA_KERNEL_SIMT, _check, lib
 
 ONELA_STATUS_PAGE, ONELA_STATUS_LENGTH, ONELA_STATUS_TIMEOUT = 1, 2, 4
 ONELA_ACT_NONE, ONELA_ACT_SIGMOID, ONELA_ACT_SILU = 0, 1, 2
@@ -165,7 +167,7 @@ def _empty(shape, dtype, index, stream, like=None):
             return torch.empty_like(like)
         return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=index)
+        stream = torch.cuda.ExternalStream(int(stream), device=index) if stream else torch.cuda.default_stream(index)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
 
@@ -227,22 +229,25 @@ def onela_paged_attention(q, k_pool, v_pool, table, lengths, beam=None, scale=No
         pmo = _arg(mass_out, "mass_out", _F32, cells, dev)
     elif mass is not None:
         raise ValueError("mass needs mass_out")
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    sizes = (R, W, H_q, H_kv, d, code, kernel, page, pages, row_pages, bpage, bpages, brow, dev, stride, scale)
-    cfg, at, need = _config(("attention", pmo is None, sizes), onela_attention_config, sizes,
-                            lambda a: lib.onela_paged_attention_scratch_bytes(a, pmo is not None))
+    pq = q.data_ptr()
     if out is None:
         o = _empty((R, W, H_q, d), dt, dev, stream, q if stride == H_q * d and q.is_contiguous() else None)
         po = o.data_ptr()
     else:
         o, po = out, _arg(out, "out", dt, (R, W, H_q, d), dev)
+    if kernel == ONELA_KERNEL_AUTO and ((pq | pk | pv) & 15 or po & 3):
+        kernel = ONELA_KERNEL_SIMT  # what the call would take, and the scratch that goes with it
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    sizes = (R, W, H_q, H_kv, d, code, kernel, page, pages, row_pages, bpage, bpages, brow, dev, stride, scale)
+    cfg, at, need = _config(("attention", pmo is None, sizes), onela_attention_config, sizes,
+                            lambda a: lib.onela_paged_attention_scratch_bytes(a, pmo is not None))
     px, nbytes = None, 0
     if scratch is not None:
         px, nbytes = _arg(scratch, "scratch", torch.uint8, scratch.shape, dev), scratch.numel()
     elif need:
         scratch = _empty((need,), torch.uint8, dev, stream)
         px, nbytes = scratch.data_ptr(), need
-    _check(lib.onela_paged_attention(at, q.data_ptr(), pk, pv, pt, pl, bk, bv, bt, bl, pm, pmo, po,
+    _check(lib.onela_paged_attention(at, pq, pk, pv, pt, pl, bk, bv, bt, bl, pm, pmo, po,
                                      _opt(lse, "lse", _F32, (R, W, H_q), dev), px, nbytes,
                                      _opt(status, "status", _I32, (1,), dev), _raw_stream(stream, dev)),
            "onela_paged_attention")

@@ -755,15 +755,10 @@ cudaError_t run(const AttnParams &p, AttnKind kind, cudaStream_t s) {
 
 bool attention_tc_supports(const onela_attention_config &c, const AttnParams &p) { return tc_fits(c, p); }
 
-size_t attention_scratch_bytes(const onela_attention_config &c, bool want_mass) {
-  // The larger of the two layouts a call may use: which kernel it takes can
-  // depend on its pointers.
-  AttnParams p = {}, g = {};
+size_t attention_scratch_bytes(const onela_attention_config &c, bool want_mass, const AttnParams &given) {
+  AttnParams p = given;
   AttnKind kind;
-  onela_attention_config general = c;
-  general.kernel = ONELA_KERNEL_SIMT;
-  const size_t a = plan_call(c, want_mass, p, nullptr, kind), b = plan_call(general, want_mass, g, nullptr, kind);
-  return a > b ? a : b;
+  return plan_call(c, want_mass, p, nullptr, kind);
 }
 
 cudaError_t launch_attention(const onela_attention_config &c, AttnParams &p, void *scratch, cudaStream_t s) {

@@ -10,7 +10,8 @@
 #include "internal.h"
 
 namespace onela {
-size_t attention_scratch_bytes(const onela_attention_config &c, bool want_mass);
+// `p`: the call's pointers, or none of them (taken to be aligned).
+size_t attention_scratch_bytes(const onela_attention_config &c, bool want_mass, const AttnParams &p);
 bool attention_tc_supports(const onela_attention_config &c, const AttnParams &p);
 cudaError_t launch_attention(const onela_attention_config &c, AttnParams &p, void *scratch, cudaStream_t s);
 }  // namespace onela
@@ -64,7 +65,8 @@ bool valid_rows(int page, int pages, int row_pages) {
 bool valid_attention(const onela_attention_config &c) {
   if (c.R < 1 || c.R > 65535 || c.W < 1 || c.H_q < 1 || c.H_kv < 1 || c.H_kv > 65535 || c.H_q % c.H_kv != 0 || c.d < 1 ||
       c.d > 256 || !valid_dtype(c.dtype) || c.kernel < ONELA_KERNEL_AUTO || c.kernel > ONELA_KERNEL_TC ||
-      !valid_rows(c.page, c.pages, c.row_pages) || c.device < 0 || !(c.scale > 0.f) || c.scale > 3.0e38f)
+      !valid_rows(c.page, c.pages, c.row_pages) || c.device < 0 || !(c.scale > 0.f) || c.scale > 2.0e38f ||
+      (long long)c.pages * c.H_kv > 0x7fffffffLL)
     return false;
   if ((long long)c.W * (c.H_q / c.H_kv) > 65536 || c.q_stride < (int64_t)c.H_q * c.d) return false;
   const bool none = c.beam_page == 0 && c.beam_pages == 0 && c.beam_row_pages == 0;
@@ -89,7 +91,7 @@ extern "C" {
 
 size_t onela_paged_attention_scratch_bytes(const onela_attention_config *cfg, int32_t want_mass) {
   if (!cfg || !valid_attention(*cfg)) return 0;
-  return onela::attention_scratch_bytes(*cfg, want_mass != 0);
+  return onela::attention_scratch_bytes(*cfg, want_mass != 0, onela::AttnParams{});
 }
 
 int onela_paged_attention(const onela_attention_config *cfg, const void *q, const void *k_pool, const void *v_pool,
@@ -111,9 +113,6 @@ int onela_paged_attention(const onela_attention_config *cfg, const void *q, cons
   for (const void *x : {(const void *)table, (const void *)lengths, (const void *)beam_table, (const void *)beam_lengths,
                         (const void *)mass, (const void *)mass_out, (const void *)lse, (const void *)status})
     if (!aligned(x, 4)) return ONELA_ERR_ARG;
-  const size_t need = onela::attention_scratch_bytes(c, mass_out != nullptr);
-  if (need > 0 && (!scratch || !aligned(scratch, 256))) return ONELA_ERR_ARG;
-  if (scratch_bytes < need) return ONELA_ERR_SCRATCH;
   onela::AttnParams p = {};
   p.q = q;
   p.k = k_pool;
@@ -130,6 +129,9 @@ int onela_paged_attention(const onela_attention_config *cfg, const void *q, cons
   p.lse = lse;
   p.status = status;
   if (c.kernel == ONELA_KERNEL_TC && !onela::attention_tc_supports(c, p)) return ONELA_ERR_UNSUPPORTED;
+  const size_t need = onela::attention_scratch_bytes(c, mass_out != nullptr, p);
+  if (need > 0 && (!scratch || !aligned(scratch, 256))) return ONELA_ERR_ARG;
+  if (scratch_bytes < need) return ONELA_ERR_SCRATCH;
   return on_device(c.device,
                    [&] { return onela::launch_attention(c, p, scratch, static_cast<cudaStream_t>(stream)); });
 }

@@ -25,7 +25,8 @@ def call_attention(L, cfg, scratch_bytes=1 << 40, **change):
 @pytest.mark.parametrize("field,value", [
     ("R", 0), ("R", 65536), ("W", 0), ("H_q", 0), ("H_q", 7), ("H_kv", 0), ("d", 0), ("d", 257), ("dtype", 2),
     ("kernel", 3), ("page", 0), ("pages", 0), ("row_pages", 0), ("row_pages", 1 << 27), ("beam_page", 1),
-    ("device", -1), ("q_stride", 511), ("scale", 0.0), ("scale", float("nan")), ("scale", float("inf")), ("W", 16385)])
+    ("device", -1), ("q_stride", 511), ("scale", 0.0), ("scale", float("nan")), ("scale", float("inf")), ("W", 16385),
+    ("pages", 1 << 30)])
 def test_attention_refuses_bad_config(field, value):
     import linear_attention_beam_shared_b200 as L
     cfg = attention(L, **{field: value})
@@ -49,6 +50,13 @@ def test_attention_refuses_missing_beam_pointers_and_small_scratch():
     need = L._lib.lib.onela_paged_attention_scratch_bytes(ctypes.addressof(cfg), 0)
     assert need > 0
     assert L._lib.lib.onela_paged_attention_scratch_bytes(ctypes.addressof(cfg), 1) > need
+    # Scores are kept only where the kernel that runs needs them.
+    wide, general = (attention(L, W=200, kernel=n) for n in (0, L.ONELA_KERNEL_SIMT))
+    rows = 2 * 200 * 8
+    sizes = [L._lib.lib.onela_paged_attention_scratch_bytes(ctypes.addressof(c), 1) for c in (wide, general)]
+    assert sizes[1] > rows * 640 * 4 > sizes[0] - 40 * rows * 64 * 4
+    # On pointers that rule the tensor cores out, the smaller scratch is refused.
+    assert call_attention(L, wide, sizes[0], q=3 * P + 2, mass_out=P) == L.ONELA_ERR_SCRATCH
     assert call_attention(L, cfg, need - 1, bk=P, bv=P, bt=P, bl=P) == L.ONELA_ERR_SCRATCH
     assert L._lib.lib.onela_paged_attention(None, *[None] * 14, 0, None, None) == L.ONELA_ERR_ARG
 

@@ -489,6 +489,47 @@ def test_block_norm_strides_in_place_and_parts():
     assert (z == 0).all() and (n == 0).all()
 
 
+def test_capture_before_any_call():
+    """In a process of its own: the first calls ever are captured, then replayed."""
+    import subprocess
+    import sys
+    code = """
+import torch, linear_attention_beam_shared_b200 as L
+i32 = dict(dtype=torch.int32, device="cuda")
+k, v = (torch.randn(40, 2, 16, 64, device="cuda").bfloat16() for _ in range(2))
+table, n = torch.arange(32, **i32)[None], torch.full((1,), 500, **i32)
+mass = torch.zeros(1, 2, 512, device="cuda")
+dst = (torch.zeros_like(k), torch.zeros_like(v), torch.arange(8, **i32)[None], torch.zeros(1, **i32), torch.zeros(1, 2, 128, device="cuda"))
+x = torch.randn(4, 256, device="cuda").bfloat16()
+w = torch.ones(256, device="cuda")
+new = torch.randn(1, 1, 2, 64, device="cuda").bfloat16()
+qs = [torch.randn(1, W, 8, 64, device="cuda").bfloat16() for W in (1, 20)] + [torch.randn(1, 2, 8, 64, device="cuda")]
+kf, vf = k.float(), v.float()
+start = torch.full((1,), 500, **i32)
+def run():
+    L.onela_cache_write(new, new, k, v, table, start)
+    o = [L.onela_paged_attention(q, *((k, v) if q.dtype == torch.bfloat16 else (kf, vf)), table, n, mass_out=mass) for q in qs]
+    L.onela_cache_evict(k, v, table, n, mass, 100, 9, *dst)
+    return o + list(L.onela_block_norm(x, x=x, w_post=w, w_pre=w))
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = run()
+g.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in out] + [t.clone() for t in dst]
+ref = run() + list(dst)
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, ref))
+raw = L.onela_paged_attention(qs[0], k, v, table, n, stream=0)
+torch.cuda.synchronize()
+assert torch.equal(raw, L.onela_paged_attention(qs[0], k, v, table, n))
+print("ok")
+"""
+    out = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and out.stdout.strip() == "ok", out.stderr[-2000:]
+
+
 @pytest.mark.parametrize("how", ["graph", "stream", "raw"])
 def test_graph_capture_and_other_streams(how):
     """All four in one captured graph, replayed on new inputs; or on a stream
