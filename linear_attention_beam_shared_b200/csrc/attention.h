@@ -54,13 +54,13 @@ __device__ __forceinline__ int prompt_len(const AttnParams &p, int r) {
 
 // The prompts, cut into tiles, are laid end to end: T tiles in all, and part
 // c of n takes tiles floor(c T / n) .. floor((c + 1) T / n) - 1 of them.  So
-// every CTA has the same work to within a tile, whatever the lengths of a batch; a
-// part may end inside one request and begin inside another.  What part c
-// finds for request r goes to slot c + r: walking along the tiles either c or
-// r grows by one at each border, so a slot has one writer, and a request's
-// slots are consecutive.  Every CTA derives the division from the lengths
-// itself (they live on the device and the host never waits for them), which
-// costs one pass over R integers.
+// every CTA has the same work to within a tile, whatever the lengths of a
+// batch; a part may end inside one request and begin inside another.  What
+// part c finds for request r goes to slot c + r: walking along the tiles
+// either c or r grows by one at each border, so a slot has one writer, and a
+// request's slots are consecutive.  Every CTA derives the division from the
+// lengths itself (they live on the device and the host never waits for them),
+// which costs one pass over R integers.
 struct PlanSmem {
   long long tot[32];
   int r;
@@ -248,8 +248,9 @@ __device__ __forceinline__ float warp_sum(float x) {
   for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
-// exp2(a - b) for a maximum b that may be -inf (nothing seen yet): 0 then.
-__device__ __forceinline__ float exp2_sub(float a, float b) { return b == -CUDART_INF_F ? 0.f : exp2f(a - b); }
+// exp2(a - b), b >= a: 0 for a = -inf, even where b is -inf too (nothing seen
+// yet); NaN stays NaN.
+__device__ __forceinline__ float exp2_sub(float a, float b) { return a == -CUDART_INF_F ? 0.f : exp2f(a - b); }
 
 // 2^x by the special-function unit (2 ulp); results below 2^-126 become 0.
 __device__ __forceinline__ float ex2(float x) {
@@ -277,10 +278,10 @@ cudaError_t launch_attn_wide(const AttnParams &p, cudaStream_t s);    // attenti
 cudaError_t launch_attn_mass_wide(const AttnParams &p, cudaStream_t s);
 
 // pdl: the kernel may be launched while the one before it in the stream still
-// runs (programmatic dependent launch).  Every kernel launched so waits for that one
-// before it touches anything the stream's earlier work may write, and lets its own
-// successor start only after that wait; so when a kernel runs, all but
-// its immediate predecessor are complete.
+// runs (programmatic dependent launch).  Every kernel launched so waits for
+// that one before it touches anything the stream's earlier work may write, and
+// lets its own successor start only after that wait; so when a kernel runs,
+// all but its immediate predecessor are complete.
 template <typename... P, typename... A>
 cudaError_t launch_kernel(void (*f)(P...), unsigned grid, unsigned threads, size_t smem, bool pdl, cudaStream_t s, A... a) {
   cudaLaunchConfig_t cfg = {};

@@ -10,7 +10,8 @@
 //     O^T += V^T P^T (16 columns of d x 8 rows, V by transposing ldmatrix),
 // P^T from the accumulators of S^T by an in-register 8 x 8 transpose.  (With the
 // rows as the 16-row side half of every product was padding: 583
-// instructions a tile of 16 tokens, and twice the time.)  Four warps each run
+// instructions a tile of 16 tokens, 47 instead of 36 us for 32 ragged requests
+// of up to 5120 tokens.)  Four warps each run
 // a ring of 16-token tiles filled by 16-byte asynchronous copies, on their
 // own (no block barrier inside a piece), and join through shared memory at
 // the end of a piece.

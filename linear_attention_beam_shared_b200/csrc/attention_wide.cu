@@ -15,8 +15,8 @@
 // buffers of 64 tokens: while a group takes the exponentials of one buffer, the
 // tensor cores fill its other one and work for the other group.  (With one
 // buffer of 128 tokens a group, each group's products waited for its
-// exponentials and these for its products: 2.3 times slower.)  The groups take
-// the two halves of 256 rows (kSub = 2, K and V read once for both) or, with at
+// exponentials and these for its products.)  The groups take the two halves of
+// 256 rows (kSub = 2, K and V read once for both) or, with at
 // most 128 rows, every other token tile of the same rows (kSub = 1), each with
 // its own result slot.  At d = 256 O fills half of the tensor memory, so there
 // is one group.
@@ -26,6 +26,11 @@
 // below 2^8, exact in range for bf16 and fp32 alike, and O is rescaled rarely.
 // P is rounded to bf16 (2^-8 relative per weight at most, of the size of the
 // rounding of o itself); its sum is that of the unrounded weights, in fp32.
+//
+// 256 beams of 16 / 4 heads of 128 take 23 us on 5120 tokens (7 of their own
+// each), two thirds of it start, partial outputs and their join, and 89 us on
+// 40960 (961 TFLOP/s; 1150 in steady state, where the scores' products, held by
+// shared memory at N = 64, take twice the outputs' time).
 //
 // Four warps bring in the K and V rows, a quarter of a tile each, through the
 // page table into rings of K and V tiles: by TMA boxes of 16 or 8 tokens

@@ -740,6 +740,27 @@ def test_attention_group_sizes(G, W):
                     mass=rng.random((2, 2, cache.row_pages * 16)).astype(np.float32))
 
 
+@pytest.mark.parametrize("dtype,d,W", [("bf16", 64, 1), ("bf16", 64, 30), ("f32", 64, 1), ("bf16", 37, 2)])
+def test_attention_nan_is_not_hidden(dtype, d, W):
+    """A NaN query gives NaN rows and weights, over a prompt, beam tokens alone, or both."""
+    import linear_attention_beam_shared_b200 as L
+    rng = np.random.default_rng(23)
+    for lengths, blen in (([300], 0), ([0], 3), ([20], 0), ([300], 3)):
+        cache = Cache(rng, lengths, 2, 16, d, dtype, row_pages=20)
+        q = rand_q(rng, 1, W, 4, d, dtype)
+        q[0, 0, 0, 0] = float("nan")
+        k, v, table, n = cache.dev()
+        beam = None
+        if blen:
+            b = draw_beam(rng, 1, W, 2, d, dtype, np.full((1, W), blen))
+            beam = (b[0], b[1], torch.from_numpy(b[2]).cuda(), torch.from_numpy(b[3]).cuda())
+        lse, m = torch.zeros(1, W, 4, device="cuda"), torch.zeros(1, 2, 320, device="cuda")
+        o = L.onela_paged_attention(q, k, v, table, n, beam=beam, lse=lse, mass_out=m)
+        assert torch.isnan(o[0, 0, 0].float()).all() and torch.isnan(lse[0, 0, 0])
+        assert torch.isfinite(o[0, 0, 1:].float()).all() and torch.isfinite(o[0, 1:].float()).all()
+        assert torch.isnan(m[0, 0, :lengths[0]]).all() and torch.isfinite(m[0, 1]).all()
+
+
 def test_attention_other_requests_nan_stays_theirs():
     """NaN in one request's query and cache leaves the others' rows alone."""
     import linear_attention_beam_shared_b200 as L
