@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kMaxThreads, kV == 4 || (kV == 2 && !kLoop) ? 
 // Any D, group, stride and alignment: one CTA per row, its values in shared
 // memory, element by element.
 __global__ void __launch_bounds__(256) block_norm_any(BlockNormParams p) {
-  extern __shared__ float buf[];  // [D] the row, then [D / group] the groups' factors
+  extern __shared__ float buf[];  // [D] the row
   __shared__ __align__(16) float red[2][32];
   int sums = 0;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(256) block_norm_any(BlockNormParams p) {
   ptx::pdl_launch_dependents();
   if (tid < 64) red[tid >> 5][tid & 31] = 0.f;
   __syncthreads();
-  float *inv = buf + p.D;
+  float inv = 1.f;  // of the one group over the whole row; smaller groups are scaled in place
   if (p.y) {
     for (int c = tid; c < p.D; c += 256) buf[c] = ld(p.y, row * p.y_stride + c, p.y_bf16);
     __syncthreads();
@@ -345,17 +345,18 @@ __global__ void __launch_bounds__(256) block_norm_any(BlockNormParams p) {
         float s = 0.f;
         for (int c = tid; c < p.D; c += 256) s += buf[c] * buf[c];
         s = block_sum(s, red, sums);
-        if (tid == 0) inv[0] = rsqrtf(s / (float)p.D + p.eps);
+        inv = rsqrtf(s / (float)p.D + p.eps);
       } else {
         for (int g = warp; g < groups; g += 8) {
           float s = 0.f;
           for (int c = lane; c < p.group; c += 32) s += buf[g * p.group + c] * buf[g * p.group + c];
 #pragma unroll
           for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          if (lane == 0) inv[g] = rsqrtf(s / (float)p.group + p.eps);
+          const float t = rsqrtf(s / (float)p.group + p.eps);
+          for (int c = lane; c < p.group; c += 32) buf[g * p.group + c] *= t;
         }
+        __syncthreads();
       }
-      __syncthreads();
     }
   }
   float s = 0.f;
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(256) block_norm_any(BlockNormParams p) {
     float t = p.x ? ld(p.x, row * p.x_stride + c, p.bf16) : 0.f;
     if (p.y) {
       float u = buf[c];
-      if (p.w_post) u = u * inv[c / p.group] * p.w_post[c % p.group];
+      if (p.w_post) u = u * inv * p.w_post[c % p.group];
       if (p.gate) u *= act(ld(p.gate, row * p.gate_stride + c, p.bf16), p.act);
       u *= p.alpha;
       if (p.scale) u *= p.scale[c];
@@ -432,7 +433,7 @@ cudaError_t launch_block_norm(const BlockNormParams &p, cudaStream_t s) {
     if (p.y_bf16) return p.bf16 ? run_types<true, true>(p, s) : run_types<true, false>(p, s);
     return p.bf16 ? run_types<false, true>(p, s) : run_types<false, false>(p, s);
   }
-  const size_t smem = (size_t)(p.D + p.D / p.group) * 4;
+  const size_t smem = (size_t)p.D * 4;
   cudaError_t e = ensure_smem_limit((const void *)block_norm_any, smem);
   if (e != cudaSuccess) return e;
   return launch_kernel(block_norm_any, (unsigned)p.N, 256, smem, true, s, p);

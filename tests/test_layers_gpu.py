@@ -433,7 +433,7 @@ def test_evict_bad_pages_and_lengths():
 
 
 NORMS = [(1, 64, 64), (5, 256, 64), (3, 2048, 2048), (2, 1000, 1000), (4, 37, 37), (3, 60, 20), (2, 8192, 8192),
-         (2, 4104, 4104), (2, 1536, 96), (1, 16384, 128), (1, 32768, 32768), (2, 5000, 8), (3, 48, 2), (700, 128, 128)]
+         (2, 4104, 4104), (2, 1536, 96), (1, 16384, 128), (1, 32768, 32768), (2, 5000, 8), (3, 48, 2), (700, 128, 128), (1, 32768, 1), (2, 30000, 3), (3, 31, 1), (1, 1, 1)]
 
 
 @pytest.mark.parametrize("parts", ["all", "heads", "post", "pre", "residual"])
