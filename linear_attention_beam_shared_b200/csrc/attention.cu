@@ -309,13 +309,18 @@ __global__ void __launch_bounds__(kThreads, 4) attn_simt(AttnParams p) {
 }
 
 // A row of d over a group of lanes, as loaded and as floats: with kD (64, 128
-// or 256) known, 8 consecutive columns for each of kD / 8 lanes; otherwise
-// columns lane + 32 i of the whole warp.
+// or 256) known, 8 consecutive columns for each of kD / 8 lanes; kD = -1: the
+// same over a whole warp for any multiple of 8; kD = 0: columns lane + 32 i of
+// the whole warp for any d and alignment.
 template <typename T, int kD>
 struct Cols {
-  static constexpr int kLanes = kD ? kD / 8 : 32;
+  static constexpr int kLanes = kD > 0 ? kD / 8 : 32;
   uint4 u[sizeof(T) / 2];
-  __device__ __forceinline__ void load(const T *row, int gl, int) {
+  __device__ __forceinline__ void load(const T *row, int gl, int d) {
+    if (kD < 0 && gl * 8 >= d) {
+      zero();
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = reinterpret_cast<const uint4 *>(row + gl * 8)[i];
   }
@@ -338,7 +343,8 @@ struct Cols {
       }
     }
   }
-  static __device__ __forceinline__ void store(T *row, int gl, int, const float (&v)[8]) {
+  static __device__ __forceinline__ void store(T *row, int gl, int d, const float (&v)[8]) {
+    if (kD < 0 && gl * 8 >= d) return;
     if constexpr (sizeof(T) == 2) {
       *reinterpret_cast<uint4 *>(row + gl * 8) =
           make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
@@ -565,29 +571,47 @@ __global__ void __launch_bounds__(kWpr == 1 ? 128 : kWpr * 32, kWpr == 1 ? (kGr 
 }
 
 // The weight each prompt position drew, from the scores the split kernel
-// stored: a thread takes four positions (kP; one where rows are no multiple
-// of 4) and adds exp2(s - lse2) over the M rows in order.
-template <int kP>
-__global__ void __launch_bounds__(kThreads) attn_mass(AttnParams p) {
-  const int chunks = (p.cap + kThreads * kP - 1) / (kThreads * kP);
-  const int pos = ((blockIdx.x % chunks) * kThreads + threadIdx.x) * kP;
+// stored: sum exp2(s - lse2) over the M rows.  A thread takes four positions
+// (kP; one where rows are no multiple of 4) and, for few rows, all of these;
+// for many the CTA's four warps take every fourth row each of the same positions
+// (kSplit = 4), joined through shared memory in a fixed order.
+template <int kP, int kSplit>
+__global__ void __launch_bounds__(kThreads) attn_mass(const __grid_constant__ AttnParams p) {
+  constexpr int kAcross = kThreads / kSplit;  // threads side by side
+  __shared__ float part[kSplit][kAcross * kP];
+  const int lane = threadIdx.x % kAcross, warp = threadIdx.x / kAcross;
+  const int chunks = (p.cap + kAcross * kP - 1) / (kAcross * kP);
+  const int first = (int)(blockIdx.x % chunks) * kAcross * kP, pos = first + lane * kP;
   const int rh = blockIdx.x / chunks, r = rh / p.Hkv;
   const int len = prompt_len(p, r);
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
-  if (pos >= len) return;
+  if (first >= len) return;
   const float *l2 = p.lse2 + (int64_t)rh * p.M, *sc = p.scores + (int64_t)rh * p.M * p.cap + pos;
   float t[kP];
 #pragma unroll
   for (int i = 0; i < kP; ++i) t[i] = 0.f;
-#pragma unroll 4
-  for (int m = 0; m < p.M; ++m) {
-    float x[kP];
-    ldn<kP, true>(sc + (int64_t)m * p.cap, x);
-    const float l = l2[m];
+  if (pos < len) {
+#pragma unroll 8
+    for (int m = warp; m < p.M; m += kSplit) {
+      float x[kP];
+      ldn<kP, true>(sc + (int64_t)m * p.cap, x);
+      const float l = l2[m];
 #pragma unroll
-    for (int i = 0; i < kP; ++i) t[i] += exp2_sub(x[i], l);
+      for (int i = 0; i < kP; ++i) t[i] += exp2_sub(x[i], l);
+    }
   }
+  if constexpr (kSplit > 1) {
+#pragma unroll
+    for (int i = 0; i < kP; ++i) part[warp][lane + kAcross * i] = t[i];
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int w = 1; w < kSplit; ++w)
+#pragma unroll
+      for (int i = 0; i < kP; ++i) t[i] += part[w][lane + kAcross * i];
+  }
+  if (pos >= len) return;
   const int64_t at = (int64_t)rh * p.cap + pos;
   if (kP == 4 && pos + 4 <= len) {
     float4 o = make_float4(t[0], t[1], t[2], t[kP - 1]);
@@ -725,6 +749,7 @@ cudaError_t run_join(const AttnParams &p, cudaStream_t s) {
     if (p.d == 64) return run_join_d<T, 64>(p, s);
     if (p.d == 128) return run_join_d<T, 128>(p, s);
     if (p.d == 256) return run_join_d<T, 256>(p, s);
+    if (p.d % 8 == 0) return run_join_d<T, -1>(p, s);
   }
   return run_join_d<T, 0>(p, s);
 }
@@ -746,9 +771,11 @@ cudaError_t run(const AttnParams &p, AttnKind kind, cudaStream_t s) {
   if (kind == kAttnWide) return launch_attn_mass_wide(p, s);
   const uintptr_t at = reinterpret_cast<uintptr_t>(p.mass) | reinterpret_cast<uintptr_t>(p.mass_out);
   const int per = p.cap % 4 == 0 && (at & 15) == 0 ? 4 : 1;
-  const unsigned grid = (unsigned)((long long)p.R * p.Hkv * ((p.cap + kThreads * per - 1) / (kThreads * per)));
-  return per == 4 ? launch_kernel(attn_mass<4>, grid, kThreads, 0, true, s, p)
-                  : launch_kernel(attn_mass<1>, grid, kThreads, 0, true, s, p);
+  const bool split = p.M > 16;
+  const int span = (split ? 32 : kThreads) * per;
+  const unsigned grid = (unsigned)((long long)p.R * p.Hkv * ((p.cap + span - 1) / span));
+  auto f = per == 4 ? (split ? attn_mass<4, 4> : attn_mass<4, 1>) : (split ? attn_mass<1, 4> : attn_mass<1, 1>);
+  return launch_kernel(f, grid, kThreads, 0, true, s, p);
 }
 
 }  // namespace

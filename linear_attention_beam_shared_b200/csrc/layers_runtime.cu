@@ -72,9 +72,9 @@ bool valid_attention(const onela_attention_config &c) {
   const bool none = c.beam_page == 0 && c.beam_pages == 0 && c.beam_row_pages == 0;
   if (!none && !valid_rows(c.beam_page, c.beam_pages, c.beam_row_pages)) return false;
   // Grids: at most one CTA per (request, token, head) row, per (request, head,
-  // 128 positions), and per (piece, head, 8 rows).
+  // 32 positions), and per (piece, head, 4 rows).
   const long long rows = (long long)c.R * c.W * c.H_q;
-  const long long pos = (long long)c.R * c.H_kv * (((long long)c.page * c.row_pages + 127) / 128);
+  const long long pos = (long long)c.R * c.H_kv * (((long long)c.page * c.row_pages + 31) / 32);
   return rows <= 0x0fffffffLL && pos <= 0x7fffffffLL;
 }
 
