@@ -64,6 +64,10 @@ def _declare() -> None:
 
 
 _declare()
+_attention, _attention_scratch = lib.onela_paged_attention, lib.onela_paged_attention_scratch_bytes
+_write, _evict, _evict_scratch = lib.onela_cache_write, lib.onela_cache_evict, lib.onela_cache_evict_scratch_bytes
+_norm = lib.onela_block_norm
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 _CODE = {torch.float32: 0, torch.bfloat16: 1}
 _CODE_OF = {**_CODE, "f32": 0, "bf16": 1}
@@ -85,11 +89,6 @@ def _arg(t, name, dtype, shape, index):
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
-
-
-def _opt(t, name, dtype, shape, index):
-    """The same for a tensor that may be None (NULL)."""
-    return None if t is None else _arg(t, name, dtype, shape, index)
 
 
 def _floats(t, name, dim):
@@ -155,7 +154,7 @@ def _row_stride(t, name, N, D):
 
 def _raw_stream(stream, index):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(index)
+        return _current_stream(index)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
@@ -225,7 +224,7 @@ def onela_paged_attention(q, k_pool, v_pool, table, lengths, beam=None, scale=No
     pm = pmo = None
     if mass_out is not None:
         cells = (R, H_kv, row_pages * page)
-        pm = _opt(mass, "mass", _F32, cells, dev)
+        pm = None if mass is None else _arg(mass, "mass", _F32, cells, dev)
         pmo = _arg(mass_out, "mass_out", _F32, cells, dev)
     elif mass is not None:
         raise ValueError("mass needs mass_out")
@@ -240,17 +239,18 @@ def onela_paged_attention(q, k_pool, v_pool, table, lengths, beam=None, scale=No
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     sizes = (R, W, H_q, H_kv, d, code, kernel, page, pages, row_pages, bpage, bpages, brow, dev, stride, scale)
     cfg, at, need = _config(("attention", pmo is None, sizes), onela_attention_config, sizes,
-                            lambda a: lib.onela_paged_attention_scratch_bytes(a, pmo is not None))
+                            lambda a: _attention_scratch(a, pmo is not None))
     px, nbytes = None, 0
     if scratch is not None:
         px, nbytes = _arg(scratch, "scratch", torch.uint8, scratch.shape, dev), scratch.numel()
     elif need:
         scratch = _empty((need,), torch.uint8, dev, stream)
         px, nbytes = scratch.data_ptr(), need
-    _check(lib.onela_paged_attention(at, pq, pk, pv, pt, pl, bk, bv, bt, bl, pm, pmo, po,
-                                     _opt(lse, "lse", _F32, (R, W, H_q), dev), px, nbytes,
-                                     _opt(status, "status", _I32, (1,), dev), _raw_stream(stream, dev)),
-           "onela_paged_attention")
+    rc = _attention(at, pq, pk, pv, pt, pl, bk, bv, bt, bl, pm, pmo, po,
+                    None if lse is None else _arg(lse, "lse", _F32, (R, W, H_q), dev), px, nbytes,
+                    None if status is None else _arg(status, "status", _I32, (1,), dev), _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "onela_paged_attention")
     return o
 
 
@@ -259,7 +259,7 @@ def onela_paged_attention_scratch_bytes(R, W, H_q, H_kv, d, dtype, page, pages, 
     """Bytes of scratch a call of these sizes needs (to keep one buffer for all of a decode's calls)."""
     c = onela_attention_config(R, W, H_q, H_kv, d, _CODE_OF[dtype], kernel, page, pages, row_pages, beam_page,
                                beam_pages, beam_row_pages, device, H_q * d, 1.0)
-    return lib.onela_paged_attention_scratch_bytes(ctypes.addressof(c), 1 if want_mass else 0)
+    return _attention_scratch(ctypes.addressof(c), 1 if want_mass else 0)
 
 
 def onela_cache_write(k, v, k_pool, v_pool, table, start, counts=None, status=None, stream=None):
@@ -275,11 +275,13 @@ def onela_cache_write(k, v, k_pool, v_pool, table, start, counts=None, status=No
     sizes = (B, n, H_kv, d, code, pool[2], pool[0], row_pages, dev, _token_stride(k, "k", (B, n, H_kv, d)),
              _token_stride(v, "v", (B, n, H_kv, d)))
     cfg, at, _ = _config(("write", sizes), onela_cache_write_config, sizes, None)
-    _check(lib.onela_cache_write(
-        at, k.data_ptr(), v.data_ptr(), _arg(k_pool, "k_pool", dt, pool, dev), _arg(v_pool, "v_pool", dt, pool, dev),
-        _arg(table, "table", _I32, (B, row_pages), dev), _arg(start, "start", _I32, (B,), dev),
-        _opt(counts, "counts", _I32, (B,), dev), _opt(status, "status", _I32, (1,), dev),
-        _raw_stream(stream, dev)), "onela_cache_write")
+    rc = _write(at, k.data_ptr(), v.data_ptr(), _arg(k_pool, "k_pool", dt, pool, dev),
+                _arg(v_pool, "v_pool", dt, pool, dev), _arg(table, "table", _I32, (B, row_pages), dev),
+                _arg(start, "start", _I32, (B,), dev),
+                None if counts is None else _arg(counts, "counts", _I32, (B,), dev),
+                None if status is None else _arg(status, "status", _I32, (1,), dev), _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "onela_cache_write")
 
 
 def onela_cache_evict(k_pool, v_pool, table, lengths, mass, keep, recent, dst_k, dst_v, dst_table, dst_lengths,
@@ -298,22 +300,24 @@ def onela_cache_evict(k_pool, v_pool, table, lengths, mass, keep, recent, dst_k,
     R = table.shape[0]
     keep, recent = int(keep), int(recent)
     sizes = (R, H_kv, d, code, page, pages, row_pages, to[0], dst_row, keep, recent, dev)
-    cfg, at, need = _config(("evict", sizes), onela_cache_evict_config, sizes, lib.onela_cache_evict_scratch_bytes)
-    pkept = _opt(kept, "kept", _I32, (R, H_kv, keep), dev)
+    cfg, at, need = _config(("evict", sizes), onela_cache_evict_config, sizes, _evict_scratch)
+    pkept = None if kept is None else _arg(kept, "kept", _I32, (R, H_kv, keep), dev)
     px, nbytes = None, 0
     if scratch is not None:
         px, nbytes = _arg(scratch, "scratch", torch.uint8, scratch.shape, dev), scratch.numel()
     elif pkept is None and need:
         scratch = _empty((need,), torch.uint8, dev, stream)
         px, nbytes = scratch.data_ptr(), need
-    _check(lib.onela_cache_evict(
+    rc = _evict(
         at, _arg(k_pool, "k_pool", dt, pool, dev), _arg(v_pool, "v_pool", dt, pool, dev),
         _arg(table, "table", _I32, (R, row_pages), dev), _arg(lengths, "lengths", _I32, (R,), dev),
         _arg(mass, "mass", _F32, (R, H_kv, row_pages * page), dev), _arg(dst_k, "dst_k", dt, to, dev),
         _arg(dst_v, "dst_v", dt, to, dev), _arg(dst_table, "dst_table", _I32, (R, dst_row), dev),
         _arg(dst_lengths, "dst_lengths", _I32, (R,), dev),
         _arg(dst_mass, "dst_mass", _F32, (R, H_kv, dst_row * page), dev), pkept, px, nbytes,
-        _opt(status, "status", _I32, (1,), dev), _raw_stream(stream, dev)), "onela_cache_evict")
+        None if status is None else _arg(status, "status", _I32, (1,), dev), _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "onela_cache_evict")
 
 
 def onela_block_norm(y=None, x=None, gate=None, gate_act="none", w_post=None, scale=None, alpha=1.0, w_pre=None,
@@ -373,9 +377,10 @@ def onela_block_norm(y=None, x=None, gate=None, gate_act="none", w_post=None, sc
     elif w_pre is not None:
         n_out = _empty((N, D), dt, dev, stream, like)
         pno = n_out.data_ptr()
-    _check(lib.onela_block_norm(at, py, pg, px, pw, _opt(scale, "scale", _F32, (D,), dev),
-                                _opt(w_pre, "w_pre", _F32, (D,), dev), pxo, pno, _raw_stream(stream, dev)),
-           "onela_block_norm")
+    rc = _norm(at, py, pg, px, pw, None if scale is None else _arg(scale, "scale", _F32, (D,), dev),
+               None if w_pre is None else _arg(w_pre, "w_pre", _F32, (D,), dev), pxo, pno, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "onela_block_norm")
     return x_out, n_out
 
 
