@@ -778,3 +778,56 @@ def test_attention_other_requests_nan_stays_theirs():
         assert torch.isnan(o[1].float()).all()
         for r in (0, 2):
             assert torch.equal(o[r], ref[r]) and torch.equal(m[r], rm[r])
+
+
+@pytest.mark.parametrize("W", [1, 24])
+def test_back_to_back_calls_see_each_other(W):
+    """A chain of dependent calls launched without a wait, each kernel allowed
+    to start while the one before it ends: bitwise what it gives with a device
+    wait after every call."""
+    import linear_attention_beam_shared_b200 as L
+    R, H_q, H, d, page, n0, steps = 2, 8, 2, 64, 16, 90, 40
+    i32 = dict(dtype=torch.int32, device="cuda")
+
+    def run(wait):
+        gen = torch.Generator(device="cuda").manual_seed(5)
+        rnd = lambda *s: torch.randn(s, generator=gen, device="cuda").bfloat16()   # noqa: E731
+        k, v = rnd(R * 20 + 1, H, page, d), rnd(R * 20 + 1, H, page, d)
+        tables = [torch.arange(R * 10, **i32).reshape(R, 10), torch.arange(R * 10, R * 20, **i32).reshape(R, 10)]
+        lens = [torch.full((R,), n0, **i32), torch.zeros(R, **i32)]
+        mass = [torch.zeros(R, H, 10 * page, device="cuda") for _ in range(2)]
+        bk, bv = rnd(R * W, H, 1, d), rnd(R * W, H, 1, d)
+        bt, bl = torch.arange(R * W, **i32).reshape(R, W, 1), torch.ones((R, W), **i32)
+        x, w = rnd(R * W, H_q * d), 1 + 0.1 * rnd(H_q * d).float()
+        sync = torch.cuda.synchronize if wait else (lambda: None)
+        torch.cuda.synchronize()
+        cur, outs = 0, []
+        for t in range(steps):
+            _, q = L.onela_block_norm(x=x, w_pre=w, want_x=False)
+            sync()
+            new = q.view(R * W, 1, H_q, d)
+            L.onela_cache_write(new[:, :, :H], new[:, :, H:2 * H], bk, bv, bt.view(R * W, 1), torch.zeros(R * W, **i32))
+            sync()
+            L.onela_cache_write(new.view(R, W, H_q, d)[:, :1, :H], new.view(R, W, H_q, d)[:, :1, H:2 * H], k, v,
+                                tables[cur], lens[cur])
+            sync()
+            lens[cur] += 1
+            o = L.onela_paged_attention(q.view(R, W, H_q, d), k, v, tables[cur], lens[cur], beam=(bk, bv, bt, bl),
+                                        mass=mass[cur], mass_out=mass[cur])
+            sync()
+            if t % 7 == 6:
+                L.onela_cache_evict(k, v, tables[cur], lens[cur], mass[cur], 80, 8, k, v, tables[1 - cur], lens[1 - cur],
+                                    mass[1 - cur])
+                sync()
+                mass[1 - cur][:, :, 80:] = 0
+                mass[cur].zero_()
+                cur = 1 - cur
+            x, _ = L.onela_block_norm(o.view(R * W, H_q * d), x=x, w_post=w, alpha=0.5)
+            sync()
+            outs.append(x)
+        torch.cuda.synchronize()
+        return outs + [k, v, lens[cur], mass[cur]]
+
+    for a, b in zip(run(True), run(False)):
+        assert torch.equal(a, b)
+        assert torch.isfinite(a.float()).all()
