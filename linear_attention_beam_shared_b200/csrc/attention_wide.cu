@@ -41,6 +41,7 @@
 #include "attention.h"
 
 #include "../../include/onela.h"
+#include "f32x2.h"
 #include "internal.h"
 #include "sm100_ptx.h"
 #include "tc_common.h"
@@ -243,16 +244,17 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
         }
         any = true;
         // The weights, over the scores' own columns.
-        const float off = mref == -CUDART_INF_F ? 0.f : mref;
-        float s4[4] = {0.f, 0.f, 0.f, 0.f};
+        const float off = mref == -CUDART_INF_F ? 0.f : -mref;
+        const F2 off2 = f2(off, off), sc2 = f2(p.scale_log2, p.scale_log2);
+        F2 s4[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           uint32_t y[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float a = ex2(fmaf(x[e >> 1][(e & 1) * 16 + 2 * i], p.scale_log2, -off));
-            const float bb = ex2(fmaf(x[e >> 1][(e & 1) * 16 + 2 * i + 1], p.scale_log2, -off));
-            s4[i & 3] += a + bb;
+            const float2 w = un(fma2(f2(x[e >> 1][(e & 1) * 16 + 2 * i], x[e >> 1][(e & 1) * 16 + 2 * i + 1]), sc2, off2));
+            const float a = ex2(w.x), bb = ex2(w.y);
+            s4[i & 3] = s4[i & 3] + f2(a, bb);
             y[i] = pack_bf16(a, bb);
           }
           ptx::tmem_st<8>(s_t + e * 8, y);
@@ -260,7 +262,8 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         ptx::mbar_arrive(&sh.p[b]);
-        sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+        const float2 sw = un((s4[0] + s4[1]) + (s4[2] + s4[3]));
+        sum += sw.x + sw.y;
       }
       tile0 += nt;
       // The outputs, unnormalised, and (maximum, sum) to the piece's slot.

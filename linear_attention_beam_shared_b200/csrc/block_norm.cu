@@ -14,6 +14,7 @@
 
 #include "../../include/onela.h"
 #include "attention.h"
+#include "f32x2.h"
 #include "internal.h"
 #include "sm100_ptx.h"
 
@@ -28,37 +29,6 @@ __device__ __forceinline__ float ld(const void *p, int64_t i, int bf16) {
 __device__ __forceinline__ void st(void *p, int64_t i, float x, int bf16) {
   if (bf16) static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(x);
   else static_cast<float *>(p)[i] = x;
-}
-
-// Two floats in one register pair: the packed fp32 instructions of sm_100 take
-// two products or sums in one issue slot, each rounded as its scalar form.
-struct F2 {
-  uint64_t u;
-};
-__device__ __forceinline__ F2 f2(float a, float b) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.u) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 un(F2 x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x.u));
-  return r;
-}
-__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
-  return r;
-}
-__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.u) : "l"(a.u), "l"(b.u), "l"(c.u));
-  return r;
 }
 
 // Eight consecutive elements, 16-byte aligned, as they lie in memory and as floats.

@@ -128,6 +128,14 @@ SHAPES = [
     (1, 70, 4, 2, 256, [500], 32),
     (2, 64, 8, 2, 128, [513, 127], 16),
     (1, 129, 4, 4, 128, [385], 48),
+    (1, 20, 8, 2, 128, [333], 8),
+    (1, 20, 8, 2, 64, [333], 24),
+    (2, 40, 8, 2, 128, [200, 90], 40),
+    (1, 40, 8, 2, 128, [200], 1),
+    (1, 24, 8, 2, 256, [150], 20),
+    (1, 17, 1, 1, 128, [5000], 16),
+    (3, 4, 8, 2, 256, [65, 64, 63], 16),
+    (1, 300, 4, 2, 64, [129], 512),
 ]
 
 
