@@ -252,12 +252,14 @@ __global__ void __launch_bounds__(kMaxThreads, kV == 4 || (kV == 2 && !kLoop) ? 
         for (int i = 0; i < 4; ++i) v[e][i] = v[e][i] * (iv * w[i]);
         if (has_g) {
           g[e].get(z);
+          // z sigmoid(z) before the product with v: v z may overflow where the gate is shut.
           if (p.act == ONELA_ACT_SILU) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[e][i] = v[e][i] * z[i];
-          }
+            for (int i = 0; i < 4; ++i) v[e][i] = v[e][i] * (z[i] * sigmoid2(z[i]));
+          } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[e][i] = v[e][i] * sigmoid2(z[i]);
+            for (int i = 0; i < 4; ++i) v[e][i] = v[e][i] * sigmoid2(z[i]);
+          }
         }
         if (has_x) {
           x[e].get(z);

@@ -839,3 +839,20 @@ def test_back_to_back_calls_see_each_other(W):
     for a, b in zip(run(True), run(False)):
         assert torch.equal(a, b)
         assert torch.isfinite(a.float()).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,D", [(2, 64), (3, 37), (2, 5000), (2400, 256)])
+def test_block_norm_shut_gates(N, D, dtype):
+    """Gates of the type's lowest value: silu and sigmoid of them are 0, whatever u is."""
+    import linear_attention_beam_shared_b200 as L
+    dt = DT[dtype]
+    y = torch.full((N, D), 30.0, device="cuda", dtype=dt)
+    y[:, ::2] = -70.0
+    x = torch.full((N, D), 2.0, device="cuda", dtype=dt)
+    gate = torch.full((N, D), torch.finfo(dt).min, device="cuda", dtype=dt)
+    w = torch.full((D,), 5.0, device="cuda")
+    for act in ("silu", "sigmoid"):
+        for post in (None, w):
+            got, _ = L.onela_block_norm(y, x=x, gate=gate, gate_act=act, w_post=post)
+            assert torch.equal(got, x)
