@@ -498,7 +498,8 @@ enum {
  * (onela_cache_write).  A row with nothing to attend to gives o = 0 and
  * lse = -inf.  Cache slots past a length are not used, whatever they hold.
  *   R, W, H_q, H_kv   >= 1; R, H_kv <= 65535, W * H_q / H_kv <= 65536, R * W *
- *                     H_q < 2^28, R * H_kv * page * row_pages < 2^36.
+ *                     H_q < 2^28, R * H_kv * page * row_pages < 2^36,
+ *                     pages * H_kv < 2^31.
  *   d                 head width, 1 .. 256.
  *   dtype             ONELA_F32 or ONELA_BF16: of q, the pools and o.
  *                     Products are accumulated and the softmax is taken in

@@ -679,16 +679,17 @@ size_t plan_call(const onela_attention_config &c, bool want_mass, AttnParams &p,
   p.row_tiles = (p.M + p.rows - 1) / p.rows;
   // Parts per (head, row tile).  n parts take ceil(groups n / ctas) waves of
   // T / n tiles and, for each, about as long as 4 tiles to start and finish;
-  // T is at most `most`.  The cheapest n, up to 8 waves.
+  // T is at most `most`.  The cheapest n, up to 8 waves: of the n with the same
+  // waves the largest is the cheapest.
   const long long groups = (long long)p.Hkv * p.row_tiles;
   const long long most = (long long)p.R * ((p.cap + p.tile - 1) / p.tile);
-  const long long limit = std::min(most, std::max(1LL, 8LL * ctas / groups));
-  double best = 0;
+  auto cost = [&](long long n) { return (double)((groups * n + ctas - 1) / ctas) * ((double)most / n + 4.0); };
+  double best = cost(1);
   p.parts = 1;
-  for (long long n = 1; n <= limit; ++n) {
-    const double cost = (double)((groups * n + ctas - 1) / ctas) * ((double)most / n + 4.0);
-    if (n == 1 || cost < best) {
-      best = cost;
+  for (long long waves = 1; waves <= 8; ++waves) {
+    const long long n = std::min(most, waves * ctas / groups);
+    if (n > 1 && cost(n) < best) {
+      best = cost(n);
       p.parts = (int)n;
     }
   }
