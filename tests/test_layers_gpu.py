@@ -856,3 +856,58 @@ def test_block_norm_shut_gates(N, D, dtype):
         for post in (None, w):
             got, _ = L.onela_block_norm(y, x=x, gate=gate, gate_act=act, w_post=post)
             assert torch.equal(got, x)
+
+
+def test_capture_of_two_branches():
+    """A captured graph whose streams part and meet: calls that follow copies,
+    clears and one another across streams; bitwise the same as plain calls."""
+    import linear_attention_beam_shared_b200 as L
+    rng = np.random.default_rng(77)
+    R, W, H_q, H, d, page = 2, 3, 8, 2, 64, 16
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cache = Cache(rng, [300, 90], H, page, d, "bf16")
+    k, v, table, lengths = cache.dev()
+    q = rand_q(rng, R, W, H_q, d, "bf16")
+    bk, bv = (torch.zeros(R * W, H, 1, d, device="cuda").bfloat16() for _ in range(2))
+    bt, one, zero = torch.arange(R * W, **i32).reshape(R, W, 1), torch.ones(R, W, **i32), torch.zeros(R * W, **i32)
+    new = rand_q(rng, R * W, 1, H, d, "bf16")
+    into, mass = torch.zeros_like(new), torch.zeros(R, H, cache.row_pages * page, device="cuda")
+    y, x = rand_q(rng, R * W, 1, 1, H_q * d, "bf16").reshape(R * W, -1), rand_q(rng, R * W, 1, 1, H_q * d, "bf16").reshape(R * W, -1)
+    w = torch.ones(H_q * d, device="cuda")
+
+    def run(main, side):
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            into.copy_(new)
+            L.onela_cache_write(into, into, bk, bv, bt.reshape(R * W, 1), zero)
+        mass.zero_()
+        _, n = L.onela_block_norm(y, x=x, w_post=w, w_pre=w)
+        main.wait_stream(side)  # the next call follows a kernel on either stream
+        o = L.onela_paged_attention(q, k, v, table, lengths, beam=(bk, bv, bt, one), mass=mass, mass_out=mass)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            bk.zero_()  # after the attention has read it
+        a, b = L.onela_block_norm(o.reshape(R * W, -1), x=n, w_post=w, w_pre=w)
+        main.wait_stream(side)
+        return o, n, a, b
+
+    side = torch.cuda.Stream()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        run(s, side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = run(torch.cuda.current_stream(), side)
+    for i in range(3):
+        new.copy_(rand_q(rng, R * W, 1, H, d, "bf16"))
+        y.copy_(rand_q(rng, R * W, 1, 1, H_q * d, "bf16").reshape(R * W, -1))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (*out, mass[:, :, :90])]
+        with torch.cuda.stream(s):
+            ref = run(s, side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, (*ref, mass[:, :, :90])))
+        assert (bk == 0).all()
