@@ -171,6 +171,15 @@ def _empty(shape, dtype, index, stream, like=None):
         return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
 
 
+def _filled(struct, sizes):
+    """The struct with these fields; ctypes would cut what does not fit one."""
+    c = struct(*sizes)
+    for (name, kind), x in zip(struct._fields_, sizes):
+        if kind is not _f32 and getattr(c, name) != x:
+            raise ValueError(f"{name} = {x} is out of range")
+    return c
+
+
 _sizes = {}
 
 
@@ -180,7 +189,7 @@ def _config(key, struct, sizes, scratch):
     if hit is None:
         if len(_sizes) >= 1024:
             _sizes.clear()
-        c = struct(*sizes)
+        c = _filled(struct, sizes)
         at = ctypes.addressof(c)
         hit = _sizes[key] = (c, at, scratch(at) if scratch else 0)
     return hit
@@ -257,8 +266,8 @@ def onela_paged_attention(q, k_pool, v_pool, table, lengths, beam=None, scale=No
 def onela_paged_attention_scratch_bytes(R, W, H_q, H_kv, d, dtype, page, pages, row_pages, beam_page=0, beam_pages=0,
                                         beam_row_pages=0, want_mass=False, kernel=ONELA_KERNEL_AUTO, device=0):
     """Bytes of scratch a call of these sizes needs (to keep one buffer for all of a decode's calls)."""
-    c = onela_attention_config(R, W, H_q, H_kv, d, _CODE_OF[dtype], kernel, page, pages, row_pages, beam_page,
-                               beam_pages, beam_row_pages, device, H_q * d, 1.0)
+    c = _filled(onela_attention_config, (R, W, H_q, H_kv, d, _CODE_OF[dtype], kernel, page, pages, row_pages, beam_page,
+                                         beam_pages, beam_row_pages, device, H_q * d, 1.0))
     return _attention_scratch(ctypes.addressof(c), 1 if want_mass else 0)
 
 

@@ -180,3 +180,21 @@ def test_binding_refuses_cpu_tensors():
         L.onela_block_norm(y=t[0, 0])
     with pytest.raises(ValueError):
         L.onela_block_norm()
+
+
+def test_binding_refuses_sizes_that_do_not_fit_their_fields():
+    """2^32 + 5 must not pass for 5."""
+    import linear_attention_beam_shared_b200 as L
+    from linear_attention_beam_shared_b200 import _layers
+    good = dict(R=1, W=1, H_q=4, H_kv=2, d=64, dtype="bf16", page=16, pages=10, row_pages=40)
+    assert L.onela_paged_attention_scratch_bytes(**good) > 0
+    for name in ("R", "W", "H_q", "pages", "row_pages"):
+        with pytest.raises(ValueError):
+            L.onela_paged_attention_scratch_bytes(**{**good, name: 2 ** 32 + good[name]})
+    sizes = [1, 2, 64, 1, 16, 10, 40, 10, 40, 100, 9, 0]
+    _layers._config(("test", tuple(sizes)), _layers.onela_cache_evict_config, sizes, None)
+    for i in (9, 10):  # keep, recent
+        bad = list(sizes)
+        bad[i] += 2 ** 32
+        with pytest.raises(ValueError):
+            _layers._config(("test", tuple(bad)), _layers.onela_cache_evict_config, bad, None)
