@@ -382,7 +382,7 @@ cudaError_t run_types(const BlockNormParams &p, cudaStream_t s) {
   auto threads = [nv](int per) { return ((nv + per - 1) / per + 31) / 32 * 32; };
   cudaError_t e;
   // Looping, two vectors a thread from 256 vectors on: fewer warps to wait for
-  // at a sum (20480 rows of 4096 in bf16: 174 us with one, 156 with two).  fp32 rows
+  // at a sum (20480 rows of 4096 in bf16: 174 us with one, 158 with two).  fp32 rows
   // in flight take twice the registers: one vector up to 512.
   if (nv <= (kYBf && kBf ? 256 : 512) ? run_loop<kYBf, kBf, 1>(p, threads(1), s, e) : nv <= 1024 && run_loop<kYBf, kBf, 2>(p, threads(2), s, e))
     return e;

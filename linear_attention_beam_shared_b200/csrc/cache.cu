@@ -132,8 +132,10 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t *warp_sums) 
 // from histograms of the keys that match so far, the cluster's added up through distributed
 // shared memory, so that every CTA finds the same digit.
 //
-// With two stretches of 16384 positions on an SM the instructions bound it (64
-// rows of 65500 positions: 27 us), so all keys are looked at three times only: when they are loaded (first
+// 64 rows of 65500 positions take 27 us, two stretches of 16384 on an SM: a
+// sixth each for the first digit's histogram, that digit, the list, the other
+// two digits, the counts and the positions, most of them ended by a barrier of the
+// cluster.  All keys are looked at three times only: when they are loaded (first
 // digit), once to list the keys of the threshold's first bin (few, unless
 // weights are nearly equal: then every key is looked at again) and count those
 // above it, and to write the positions.  Positions past the row have key 0,
