@@ -911,3 +911,52 @@ def test_capture_of_two_branches():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, (*ref, mass[:, :, :90])))
         assert (bk == 0).all()
+
+
+def test_threads_on_streams_of_their_own():
+    """Calls of all kinds from four host threads at once, bitwise as from one."""
+    import threading
+    import linear_attention_beam_shared_b200 as L
+    rng = np.random.default_rng(78)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    jobs = []
+    for W in (1, 3, 20, 40):
+        cache = Cache(rng, [500, 33], 2, 16, 64, "bf16")
+        jobs.append((rand_q(rng, 2, W, 8, 64, "bf16"), cache.dev(), rand_q(rng, 2, 1, 2, 64, "bf16")))
+    w = torch.ones(512, device="cuda")
+    torch.cuda.synchronize()
+
+    def run(i, into, stream):
+        q, (k, v, table, lengths), new = jobs[i]
+        with torch.cuda.stream(stream):
+            mass = torch.zeros(2, 2, table.shape[1] * 16, device="cuda")
+            kk, vv = k.clone(), v.clone()
+            L.onela_cache_write(new, new, kk, vv, table, lengths - 1)
+            o = L.onela_paged_attention(q, kk, vv, table, lengths, mass_out=mass)
+            dst = [torch.zeros(8, 2, 16, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+            n, m = torch.zeros(2, **i32), torch.zeros(2, 2, 64, device="cuda")
+            L.onela_cache_evict(kk, vv, table, lengths, mass, 50, 7, *dst, torch.arange(8, **i32).reshape(2, 4), n, m)
+            x, y = L.onela_block_norm(o.reshape(-1, 512), w_post=w, w_pre=w)
+        stream.synchronize()
+        into[i] = [o, mass, *dst, n, m, x, y]
+
+    ref, errors = {}, []
+    for i in range(4):
+        run(i, ref, torch.cuda.current_stream())
+
+    def many(i):
+        try:
+            stream, got = torch.cuda.Stream(), {}
+            for _ in range(20):
+                run(i, got, stream)
+                if not all(torch.equal(a, b) for a, b in zip(got[i], ref[i])):
+                    errors.append(f"job {i} differs")
+        except Exception as e:  # noqa: BLE001
+            errors.append(repr(e))
+
+    threads = [threading.Thread(target=many, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
