@@ -41,6 +41,7 @@
 #include "attention.h"
 
 #include "../../include/onela.h"
+#include "copy_reports.h"
 #include "f32x2.h"
 #include "internal.h"
 #include "sm100_ptx.h"
@@ -311,19 +312,16 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
     const uint8_t *kp = static_cast<const uint8_t *>(p.k), *vp = static_cast<const uint8_t *>(p.v);
     const bool one_page = p.page % 16 == 0;
     uint32_t it = 0;             // items (K and V tiles in turn) issued
-    uint32_t told = 0, pend = 0;  // items reported full, and which of the others are for this warp to report
+    CopyReports rep;             // which of them this warp has to report full
     auto full_bar = [&](uint32_t i) { return (i & 1) ? &sh.vfull[(i >> 1) % NS] : &sh.kfull[(i >> 1) % NS]; };
     // Asynchronous copies that have landed become visible to the tensor cores' reads.
     auto tell = [&](uint32_t upto) {
-      if (told < upto && pend) {
-        ptx::fence_proxy_async();
-        __syncwarp();
-        for (; told < upto; ++told) {
-          if (lane == 0 && ((pend >> (told & 31)) & 1)) ptx::mbar_arrive(full_bar(told));
-          pend &= ~(1u << (told & 31));
-        }
-      }
-      told = upto;
+      if (!rep.due(upto)) return;
+      ptx::fence_proxy_async();
+      __syncwarp();
+      rep.landed(upto, [&](uint32_t i) {
+        if (lane == 0) ptx::mbar_arrive(full_bar(i));
+      });
     };
     while (walk.next(p)) {
       const int32_t *tab = p.table + (int64_t)walk.r * p.row_pages;
@@ -362,7 +360,7 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
           uint64_t *empty = kv ? &sh.vempty[st] : &sh.kempty[st];
           if (n > 0 && !dead && !__all_sync(0xffffffffu, ptx::mbar_try_wait(empty, (n - 1) & 1))) {
             // Nothing to issue yet: hand over all that is under way first.
-            if (pend) {
+            if (rep.pend) {
               cp_wait<0>();
               tell(it);
             }
@@ -393,10 +391,10 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
               ptx::cp_async16(dst + (cc >> 3) * (TT * 128) + ptx::swz128(lw * kTokW + tk, cc & 7), src + off,
                               sph < 0 ? 0 : 16);
             }
-            pend |= 1u << (it & 31);
+            rep.mark(it);
           }
           ptx::cp_async_commit();
-          if (pend && it >= 2) {
+          if (rep.pend && it >= 2) {
             cp_wait<2>();
             tell(it - 1);
           }

@@ -1,0 +1,151 @@
+"""Paged attention where a CTA walks many tiles of a row, or a row is cut into
+many pieces, against the definition in 64 bits on the device: o, lse and the
+weights drawn.
+
+Bounds, per element, before any run.  With u = 2^-23 (unit of the fp32 sums: the
+tensor cores may truncate where an FMA rounds):
+  a score is a d-term sum, off by at most e = scale (d + 4) u max |q| |k|, and
+  the argument of exp2 (score minus reference) is rounded: top u each, top the
+  largest |score|;
+  the weights of a row are summed in tiles of at most 64 tokens (four chains or
+  fewer: counted as 64 terms), over the tiles of a CTA, then over its pieces:
+  m = 64 + tiles + pieces terms one after another, not the row's length;
+  so a weight is off, relative to itself, by rel = 2 e + 2 top u + m u + 2^-20
+  (exp2 is within 2 ulp; the division), and with bf16 also by P's rounding, 2^-8;
+  o sums the same way (m u more):
+  |o - ref| <= sum p|v| (rel + m u + 2^-8) + half a step of o,
+  |lse - ref| <= rel + |lse| 2^-22,
+  |drawn - ref| <= drawn (rel + rows u) + 2^-23 |mass|.
+"""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -23
+
+
+def build(gen, lengths, H, page, d, dtype, bad=()):
+    """Pools with scattered pages, NaN where no token lies; bad: (request,
+    table entry) pairs whose page number is out of range."""
+    R = len(lengths)
+    row_pages = -(-max(lengths) // page)
+    pages = R * row_pages + 1
+    k, v = (torch.randn((pages, H, page, d), generator=gen, device="cuda").to(dtype) for _ in range(2))
+    table = torch.randperm(pages, generator=gen, device="cuda")[:R * row_pages].to(torch.int32).reshape(R, row_pages)
+    for r, n in enumerate(lengths):
+        for e in range(n // page, row_pages):
+            at = max(0, n - e * page)
+            k[table[r, e].long(), :, at:] = float("nan")
+            v[table[r, e].long(), :, at:] = float("nan")
+    shown = table.clone()
+    for r, e in bad:
+        shown[r, e] = pages + 5
+    return k, v, table, shown
+
+
+def reference(q, k, v, table, shown, lengths, scale, mass):
+    """o, lse, drawn + mass, sum p|v| and the largest |score| in 64 bits."""
+    R, W, H_q, d = q.shape
+    pages, H, page, _ = k.shape
+    G = H_q // H
+    o, spread = torch.zeros(R, W, H_q, d, dtype=torch.float64, device="cuda"), torch.zeros(R, W, H_q, d, dtype=torch.float64, device="cuda")
+    lse = torch.full((R, W, H_q), -float("inf"), dtype=torch.float64, device="cuda")
+    drawn = mass.double().clone()
+    top = 0.0
+    for r, n in enumerate(lengths):
+        j = torch.arange(n, device="cuda")
+        entry = shown[r].long()[j // page]
+        live = (entry >= 0) & (entry < pages)
+        j = j[live]
+        if not len(j):
+            continue
+        at = table[r].long()[j // page]
+        for h in range(H):
+            kk, vv = k[at, h, j % page].double(), v[at, h, j % page].double()
+            qq = q[r, :, h * G:(h + 1) * G].double()
+            s = torch.einsum("wgd,nd->wgn", qq, kk) * scale
+            top = max(top, float(s.abs().max()))
+            l = torch.logsumexp(s, -1)
+            p = torch.exp(s - l[..., None])
+            o[r, :, h * G:(h + 1) * G] = torch.einsum("wgn,nd->wgd", p, vv)
+            spread[r, :, h * G:(h + 1) * G] = torch.einsum("wgn,nd->wgd", p, vv.abs())
+            lse[r, :, h * G:(h + 1) * G] = l
+            drawn[r, h, j] += p.sum((0, 1))
+    return o, lse, drawn, spread, top
+
+
+def check(q, k, v, table, shown, lengths, tiles, pieces, kernel=0, scale=None):
+    import linear_attention_beam_shared_b200 as L
+    R, W, H_q, d = q.shape
+    H, page = k.shape[1:3]
+    scale = d ** -0.5 if scale is None else scale
+    cap = table.shape[1] * page
+    mass = torch.rand((R, H, cap), device="cuda")
+    mass_out = torch.full_like(mass, -3.0)
+    lse = torch.full((R, W, H_q), 7.0, device="cuda")
+    n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    o = L.onela_paged_attention(q, k, v, shown, n, scale=scale, mass=mass, mass_out=mass_out, lse=lse, kernel=kernel)
+    ro, rl, rm, spread, top = reference(q, k, v, table, shown, lengths, scale, mass)
+    qn = float(q.double().square().sum(-1).max().sqrt())
+    kn = float(torch.nan_to_num(k.double(), nan=0.0).square().sum(-1).max().sqrt())
+    m = 64 + tiles + pieces
+    rel = 2 * scale * (d + 4) * U * qn * kn + 2 * top * U + m * U + 2.0 ** -20
+    bf = 2.0 ** -8 if q.dtype == torch.bfloat16 else 0.0
+    half = 2.0 ** -8 if q.dtype == torch.bfloat16 else 2.0 ** -24
+    lim = 1.01 * (spread * (rel + m * U + bf) + half * ro.abs()) + 1e-30
+    err = (o.double() - ro).abs()
+    assert bool((err <= lim).all()), f"o: {float((err / lim).max())} of its bound"
+    err, lim = (lse.double() - rl).abs(), rel + rl.abs() * 2.0 ** -22
+    fin = torch.isfinite(rl)
+    assert bool((torch.isneginf(lse) == torch.isneginf(rl)).all())
+    assert bool((err[fin] <= lim[fin]).all()), f"lse: {float((err / lim)[fin].max())} of its bound"
+    for r, c in enumerate(lengths):
+        assert bool((mass_out[r, :, c:] == -3.0).all())
+        a, b = mass_out[r, :, :c].double(), rm[r, :, :c]
+        err, lim = (a - b).abs(), 1.01 * (b - mass[r, :, :c].double()) * (rel + W * H_q // H * U) + b * 2.0 ** -23
+        assert bool((err <= lim).all()), f"weights: {float((err / lim).max())} of their bound"
+    return o, lse, mass_out
+
+
+# One part per head (148 key-value heads fill the SMs), so a CTA walks the whole
+# row: 17, 35 or 58 tiles of 64, the last one not full.
+@pytest.mark.parametrize("page", [8, 16, 20])
+@pytest.mark.parametrize("W,G,d", [(20, 1, 64), (11, 6, 128), (64, 4, 64), (75, 4, 128), (5, 8, 256)])
+@pytest.mark.parametrize("tiles,left", [(17, 5), (35, 63), (58, 1)])
+def test_a_partly_filled_tile_behind_many_full_ones(tiles, left, W, G, d, page):
+    """The last tokens carry the weight: K's rows there lie along the queries'
+    common direction, so a score of other rows shows."""
+    gen = torch.Generator(device="cuda").manual_seed(tiles * W + page)
+    H, n = 148, 64 * (tiles - 1) + left
+    k, v, table, shown = build(gen, [n], H, page, d, torch.bfloat16)
+    u = torch.sign(torch.randn((H, d), generator=gen, device="cuda"))
+    q = (torch.randn((1, W, H, G, d), generator=gen, device="cuda") * 0.5 + u[None, None, :, None]).reshape(1, W, H * G, d).bfloat16()
+    last = torch.arange(n - left, n, device="cuda")
+    at = table[0].long()[last // page]
+    boost = 6.0 * d ** -0.5  # adds 6 to these tokens' scores
+    k[at, :, last % page] = (k[at, :, last % page].float() + boost * u).bfloat16()
+    check(q, k, v, table, shown, [n], tiles, 1)
+
+
+@pytest.mark.parametrize("page", [8, 16])
+@pytest.mark.parametrize("W,G,d", [(20, 1, 64), (64, 4, 128)])
+def test_a_bad_page_behind_many_full_tiles(W, G, d, page):
+    """Tiles 20 and 40 of 50 miss a page's tokens."""
+    gen = torch.Generator(device="cuda").manual_seed(W + page)
+    H, n = 148, 64 * 50
+    k, v, table, shown = build(gen, [n], H, page, d, torch.bfloat16, bad=[(0, 20 * 64 // page + 1), (0, 40 * 64 // page)])
+    q = torch.randn((1, W, H * G, d), generator=gen, device="cuda").bfloat16()
+    check(q, k, v, table, shown, [n], 50, 1)
+
+
+@pytest.mark.parametrize("lengths,W,H_q,H,d,tiles,pieces", [
+    ([65541], 32, 32, 8, 128, 57, 19), ([4999] * 8, 8, 32, 8, 128, 40, 4), ([4990 + 3 * r for r in range(9)], 16, 16, 8, 64, 40, 4),
+    ([9000, 70, 1, 12000, 0, 333], 70, 8, 4, 128, 40, 37)])
+def test_parts_that_cross_requests(lengths, W, H_q, H, d, tiles, pieces):
+    """Parts of many tiles that end inside a request, begin inside the next,
+    and meet partly filled tiles on the way."""
+    gen = torch.Generator(device="cuda").manual_seed(len(lengths))
+    k, v, table, shown = build(gen, lengths, H, 16, d, torch.bfloat16)
+    q = torch.randn((len(lengths), W, H_q, d), generator=gen, device="cuda").bfloat16()
+    check(q, k, v, table, shown, lengths, tiles, pieces)
