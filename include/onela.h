@@ -334,10 +334,12 @@ ONELA_API int onela_reset(onela_handle *h, onela_stream stream);
  * Runs on the device only (no host synchronisation; capturable in a CUDA
  * graph: the prompt state is never overwritten, so a captured decode that
  * folds replays from the prompt each time).  Tensor-core handles with
- * d_k = d_v <= 128 and T_max <= 16 fold in one launch that overlaps the
- * steps around it: it starts once the step before it is complete, and a
- * step launched while it runs replays from the root state before the fold
- * (which the fold leaves alone) where those depths still fit the record
+ * d_k = d_v <= 128 and T_max <= 16 fold in one launch that overlaps the step
+ * before it: it starts once that step is complete.  Under ONELA_FLAG_PDL it
+ * overlaps the step after it too (without the flag that step is an ordinary
+ * launch, so its inputs may be written by any kernel between the two): a
+ * step launched while the fold runs replays from the root state before the
+ * fold (which the fold leaves alone) where those depths still fit the record
  * store, else it waits for the fold; the outputs are the same either way up
  * to rounding.  Other handles fold in ordinary launches, and the next step
  * is an ordinary launch too.  Memory: a second state buffer and, tensor-core

@@ -418,17 +418,21 @@ int decode_one(onela_handle *h, int32_t W_prev, int32_t W, const void *q, const 
   p.o = o;
   cudaError_t e;
   const bool contract = (c.flags & ONELA_FLAG_PDL) != 0;
-  // A step overlaps the step before it under ONELA_FLAG_PDL, or inside one
-  // onela_decode_steps call when the depth its early writes replace
-  // (t - T_max) is none, or of the same call (then no step still running
-  // reads it from the store).  The tensor-core step right after a fold
+  // A programmatic step reads its inputs before it waits for the kernel
+  // before it in the stream, so it needs to know that this kernel writes none
+  // of them: by the contract of ONELA_FLAG_PDL, or as a later step of one
+  // onela_decode_steps call (the kernel before it is then a step), when the
+  // depth its early writes replace (t - T_max) is none, or of the same call
+  // (then no step still running reads it from the store).  A fold before the
+  // step does not tell: any kernel may lie between the two, and the operators
+  // around a GDN layer let their successors start before they have written.
+  // Under the contract the tensor-core step right after a one-launch fold
   // overlaps the fold: it replays from the folded state before that fold
   // (which the fold does not write) where that still fits the record store,
-  // and waits for the fold elsewhere (StepParams::after_fold).
+  // and waits for the fold elsewhere (StepParams::fold_pending).
   const int tr = p.t - c.T_max;
   const bool in_call = call_t0 > 0 && p.t > call_t0 && (tr < 1 || tr >= call_t0);
-  const bool after_fold = h->after_fold && h->fold_pending;  // after the one-launch tensor-core fold
-  const bool pdl = p.t >= 2 && (after_fold || (!h->after_fold && (contract || in_call)));
+  const bool pdl = p.t >= 2 && (contract || in_call) && (!h->after_fold || h->fold_pending);
   if (p.t == 1 && h->kernel == ONELA_KERNEL_TC) p.fold_reset = h->fold_buf + (2 + c.T_max) * c.R;
   if (h->fold_pending && h->kernel == ONELA_KERNEL_TC) {
     p.fold_pending = 1;
