@@ -96,7 +96,9 @@ enum {
  *                   decode steps whose inputs were all written before the
  *                   first of them, as in a CUDA graph of a whole decode, or
  *                   the verification of a tree of drafted tokens.  Step 1
- *                   never overlaps. */
+ *                   never overlaps, nor does a step before which one of the
+ *                   operators around a GDN layer (below) was called since
+ *                   the handle's last step or fold. */
 enum { ONELA_FLAG_PDL = 1 };
 /*   ONELA_FLAG_NVTX  mark every decode step, fold and prefill call on the
  *                   host with an NVTX range ("onela step t", ...) for

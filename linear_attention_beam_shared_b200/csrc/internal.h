@@ -134,6 +134,15 @@ inline int32_t err_bits(int32_t raw) {
 // repeated inside a captured region.  Safe to call from several host threads.
 cudaError_t ensure_smem_limit(const void *func, size_t smem);
 
+// Calls of the operators around a GDN layer that launched so far, in this
+// process (layers_runtime.cu).  Their kernels let their successors start
+// before they have written, and a step that starts as a programmatic dependent
+// lets its own start before it has waited: a step launched so right behind an
+// operator could bring the step after it, which may read what the operator
+// writes, beside that operator.  The handle compares this number at two of its
+// calls to know that no operator was launched between them.
+uint64_t operator_calls();
+
 // Kernel launchers (step_simt.cu, step_tc.cu).  Return a cudaError_t.
 cudaError_t launch_step_simt(const StepParams &p, int qkv_bf16, int s0_bf16, cudaStream_t s);
 cudaError_t launch_step_tc(const StepParams &p, int pdl, cudaStream_t s);

@@ -1,7 +1,9 @@
 // Entry points of the operators around a GDN layer (include/onela.h): checks
 // of the arguments on the host, then the launches.  Nothing is kept between
-// calls and nothing is allocated.
+// calls but their number, and nothing is allocated.
 #include <cuda_runtime.h>
+
+#include <atomic>
 
 #include "../../include/onela.h"
 #include "attention.h"
@@ -17,6 +19,8 @@ cudaError_t launch_attention(const onela_attention_config &c, AttnParams &p, voi
 }  // namespace onela
 
 namespace {
+
+std::atomic<uint64_t> g_calls{0};
 
 bool valid_dtype(int d) { return d == ONELA_F32 || d == ONELA_BF16; }
 size_t esize(int d) { return d == ONELA_BF16 ? 2 : 4; }
@@ -46,6 +50,7 @@ int on_device(int device, F f) {
   try {
     DeviceGuard g(device);
     if (!g.ok) return ONELA_ERR_CUDA;
+    g_calls.fetch_add(1, std::memory_order_relaxed);  // calls on one stream are ordered by their caller
     if (f() != cudaSuccess) {
       cudaGetLastError();
       return ONELA_ERR_CUDA;
@@ -86,6 +91,8 @@ bool valid_evict(const onela_cache_evict_config &c) {
 }
 
 }  // namespace
+
+uint64_t onela::operator_calls() { return g_calls.load(std::memory_order_relaxed); }
 
 extern "C" {
 

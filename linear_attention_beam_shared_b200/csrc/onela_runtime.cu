@@ -35,6 +35,7 @@ struct onela_handle {
   int folded;      // S0f and fold_buf are in use since the last rewind
   int fold_cur;    // which d0 buffer holds the current depths
   int after_fold;  // the last call was a fold
+  uint64_t operators;  // operator_calls() at the last step or fold
   int fold_prev;   // a fold came before the last one since the rewind (its depth and image are the old ones)
   // The last fold was the one-launch tensor-core fold, whose CTAs count
   // themselves done in fold_buf's done counters ([R], zeroed by step 1 of
@@ -432,7 +433,12 @@ int decode_one(onela_handle *h, int32_t W_prev, int32_t W, const void *q, const 
   // and waits for the fold elsewhere (StepParams::fold_pending).
   const int tr = p.t - c.T_max;
   const bool in_call = call_t0 > 0 && p.t > call_t0 && (tr < 1 || tr >= call_t0);
-  const bool pdl = p.t >= 2 && (contract || in_call) && (!h->after_fold || h->fold_pending);
+  // The contract speaks of the kernel before the step, not of the operators
+  // around a GDN layer that came before a run of steps: behind one of those the
+  // step is an ordinary launch (operator_calls).
+  const uint64_t operators = onela::operator_calls();
+  const bool overlaps = (contract && h->operators == operators) || in_call;
+  const bool pdl = p.t >= 2 && overlaps && (!h->after_fold || h->fold_pending);
   if (p.t == 1 && h->kernel == ONELA_KERNEL_TC) p.fold_reset = h->fold_buf + (2 + c.T_max) * c.R;
   if (h->fold_pending && h->kernel == ONELA_KERNEL_TC) {
     p.fold_pending = 1;
@@ -489,6 +495,7 @@ int decode_one(onela_handle *h, int32_t W_prev, int32_t W, const void *q, const 
   }
   h->steps_done += 1;
   h->after_fold = 0;
+  h->operators = operators;
   h->last_launches = 1;
   h->Ws.push_back(W);
   h->hist_k.push_back(k);
@@ -623,6 +630,7 @@ int onela_fold(onela_handle *h, int32_t max_depth, onela_stream stream) {
   h->fold_prev = h->folded;
   h->folded = 1;
   h->after_fold = 1;
+  h->operators = onela::operator_calls();  // the fold waits before it lets the next step start
   h->fold_pending = pending;
   return ONELA_OK;
 }

@@ -80,3 +80,64 @@ def test_step_after_a_fold_sees_the_norms_between(captured, T_max):
     for _ in range(3):
         for t, (a, b) in enumerate(zip(want, run(False, captured))):
             assert torch.equal(a, b), f"step {t + 1}"
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_flagged_steps_behind_a_norm_that_feeds_a_later_one(captured):
+    """ONELA_FLAG_PDL: before step t a norm writes the q of step t + 1, so the
+    kernel before each step produces no input of that step; k, gates and parents
+    stay as they are throughout."""
+    import linear_attention_beam_shared_b200 as L
+    R, H, d, W, T = 4, 16, 128, 256, 12
+    S0, steps = draw(4, R, H, d, W, T)
+    w = torch.ones(d, device="cuda") * d ** -0.5
+    shape = (R, W, H, d)
+    for s in steps:
+        s["k"], s["v"] = ((s[n] * d ** -0.5).bfloat16().view(shape) for n in ("k", "v"))
+        s["g"] = s["g"].view(R, W, H)
+
+    def run(wait, graph=False):
+        sync = torch.cuda.synchronize if wait else (lambda: None)
+        dec = L.BeamDecoder(R, H, d, d, W, T, "f32", "bf16", flags=L.ONELA_FLAG_PDL)
+        q = [torch.zeros((R * W * H, d), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        outs = [torch.zeros(shape, device="cuda") for _ in range(T)]
+
+        def chain():
+            L.onela_block_norm(steps[0]["q"], w_post=w, dtype="bf16", x_out=q[0])
+            sync()
+            for t, s in enumerate(steps):
+                if t + 1 < T and t % 2 == 0:  # before steps 1, 3, 5, ..: the q of the step after
+                    L.onela_block_norm(steps[t + 1]["q"], w_post=w, dtype="bf16", x_out=q[(t + 1) % 2])
+                    sync()
+                dec.step(q[t % 2].view(shape), s["k"], s["v"], s["g"], s["beta"], s["par"], o=outs[t])
+                sync()
+                if t + 1 < T and t % 2 == 1:  # the q of the next step, and a norm of no step's behind it
+                    L.onela_block_norm(steps[t + 1]["q"], w_post=w, dtype="bf16", x_out=q[(t + 1) % 2])
+                    sync()
+                    L.onela_block_norm(steps[0]["g"].view(R * W, H), alpha=2.0)
+                    sync()
+        try:
+            dec.set_prompt_state(S0)
+            torch.cuda.synchronize()
+            if graph:
+                g = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(g):
+                    chain()
+                g.replay()
+                torch.cuda.synchronize()
+                for o in outs:
+                    o.zero_()
+                g.replay()
+            else:
+                chain()
+            torch.cuda.synchronize()
+            assert dec.status() == 0
+            return outs
+        finally:
+            torch.cuda.synchronize()
+            dec.close()
+
+    want = run(True)
+    for _ in range(3):
+        for t, (a, b) in enumerate(zip(want, run(False, captured))):
+            assert torch.equal(a, b), f"step {t + 1}"
