@@ -93,14 +93,12 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// Wait unless a wait of this thread has run out before.
-__device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, bool &dead) {
-  if (!dead && !ptx::mbar_wait(bar, parity, kWaitNs)) dead = true;
-}
-// The same by a whole warp, which goes on together.
+// Wait of a whole warp, which goes on together and alike: `dead` is the same in
+// all its lanes (a barrier may complete between two lanes' last looks at it).
+// No wait once one has run out.
 __device__ __forceinline__ void wait_warp(uint64_t *bar, uint32_t parity, bool &dead) {
-  wait(bar, parity, dead);
-  __syncwarp();
+  if (!dead && !ptx::mbar_wait(bar, parity, kWaitNs)) dead = true;
+  dead = __any_sync(0xffffffffu, dead);
 }
 
 template <int D, int kSub>
@@ -364,8 +362,7 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
               cp_wait<0>();
               tell(it);
             }
-            wait(empty, (n - 1) & 1, dead);
-            dead = __any_sync(0xffffffffu, dead);  // the warp stays together
+            wait_warp(empty, (n - 1) & 1, dead);
           }
           if (kv == 0 && lane == 0) sh.mask[(it >> 1) & 7][lw] = here;
           uint8_t *dst = smem + (kv ? C::oV : C::oK) + st * C::kTile;
@@ -626,7 +623,6 @@ __global__ void __launch_bounds__(MassCfg<D>::kThreads, D == 256 ? 1 : 2) attn_m
     for (int t = 0; t < nt; ++t) {
       const int st = t % NS;
       if (t >= NS) wait_warp(&sh.empty[st], (t / NS - 1) & 1, dead);
-      dead = __any_sync(0xffffffffu, dead);
       uint8_t *dst = smem + C::kK + st * C::kTile;
       const int m = t * 64 + lw * 16 + lane;  // lanes 0 .. 15: this warp's rows
       const int64_t mine = lane < 16 && m < p.M
