@@ -461,8 +461,8 @@ ONELA_API int onela_decode_step_noalloc(const onela_config *cfg, int32_t t, int3
  * prompt part the beams of a request share, writing to that cache, evicting
  * from it, and the norms around a block.
  *
- * They hold no handle and keep nothing between calls.  Their conventions are
- * those above; in addition
+ * They hold no handle and keep nothing of a call for the next.  Their
+ * conventions are those above; in addition
  *   - `scratch` is a DEVICE buffer on a 256-byte boundary, owned by the
  *     caller and borrowed for the stream-ordered duration of the call.  Its
  *     contents need not be kept or cleared between calls; calls that may run
@@ -559,6 +559,18 @@ ONELA_API int onela_paged_attention(const onela_attention_config *cfg, const voi
                                     const int32_t *beam_lengths, const float *mass, float *mass_out, void *o,
                                     float *lse, void *scratch, size_t scratch_bytes, int32_t *status,
                                     onela_stream stream);
+
+/* Bound of every wait of the attention's tensor-core kernels (many query rows)
+ * on another of their warp roles, for all later calls of the process: limit_ns
+ * in [1e6, 1e10] nanoseconds, default 2e9.  A wait that runs out sets
+ * ONELA_STATUS_TIMEOUT; the kernel then ends without the missing data, and the
+ * rows and positions concerned are NaN.  stall != 0 is a testing aid: one kind
+ * of barrier then expects an arrival that never comes, so that the waits on it
+ * run out at the bound (nothing faults or hangs): of the attention 1 stages to
+ * refill, 2 stages filled, 3 scores, 4 weights, 5 outputs; of the drawn weights 6
+ * stages to refill, 7 stages filled, 8 scores, 9 score buffers read.  0 restores
+ * normal operation.  Errors: ONELA_ERR_ARG. */
+ONELA_API int onela_set_attention_wait_policy(uint64_t limit_ns, int32_t stall);
 
 /* Write tokens to the cache: row b's token i (i < n, and i < counts[b] if
  * counts is given) goes to position start[b] + i of table row b.

@@ -33,6 +33,7 @@ from ._lib import (  # noqa: F401
 from ._layers import (  # noqa: F401
     ONELA_ACT_NONE, ONELA_ACT_SIGMOID, ONELA_ACT_SILU, ONELA_STATUS_LENGTH, ONELA_STATUS_PAGE, ONELA_STATUS_TIMEOUT,
     onela_block_norm, onela_cache_evict, onela_cache_write, onela_paged_attention, onela_paged_attention_scratch_bytes,
+    onela_set_attention_wait_policy,
 )
 
 LIB_PATH = _lib.LIB_PATH

@@ -53,6 +53,7 @@ def _declare() -> None:
     sig = {
         "onela_paged_attention_scratch_bytes": ([_vp, _i32], ctypes.c_size_t),
         "onela_paged_attention": ([_vp] * 15 + [ctypes.c_size_t, _vp, _vp], ctypes.c_int),
+        "onela_set_attention_wait_policy": ([ctypes.c_uint64, _i32], ctypes.c_int),
         "onela_cache_write": ([_vp] * 10, ctypes.c_int),
         "onela_cache_evict_scratch_bytes": ([_vp], ctypes.c_size_t),
         "onela_cache_evict": ([_vp] * 13 + [ctypes.c_size_t, _vp, _vp], ctypes.c_int),
@@ -269,6 +270,12 @@ def onela_paged_attention_scratch_bytes(R, W, H_q, H_kv, d, dtype, page, pages, 
     c = _filled(onela_attention_config, (R, W, H_q, H_kv, d, _CODE_OF[dtype], kernel, page, pages, row_pages, beam_page,
                                          beam_pages, beam_row_pages, device, H_q * d, 1.0))
     return _attention_scratch(ctypes.addressof(c), 1 if want_mass else 0)
+
+
+def onela_set_attention_wait_policy(limit_ns: int, stall: int = 0) -> None:
+    """Bound of the waits inside the attention's tensor-core kernels, for the
+    whole process (see onela.h); stall is a testing aid."""
+    _check(lib.onela_set_attention_wait_policy(int(limit_ns), int(stall)), "onela_set_attention_wait_policy")
 
 
 def onela_cache_write(k, v, k_pool, v_pool, table, start, counts=None, status=None, stream=None):

@@ -45,6 +45,14 @@ struct AttnParams {
   float2 *part_ml;
   float *lse2;
   float *scores;
+  // Of the tensor-core kernel's waits between its warps: the bound of each, and
+  // (tests) the barriers that expect one arrival more than will come.
+  unsigned long long wait_ns;
+  int stall;  // 0 or kStall*
+};
+enum {
+  kStallEmpty = 1, kStallFull, kStallScores, kStallWeights, kStallOutputs,       // attn_wide
+  kStallMassEmpty, kStallMassFull, kStallMassScores, kStallMassRead, kStallEnd  // attn_mass_wide
 };
 
 __device__ __forceinline__ int prompt_len(const AttnParams &p, int r) {

@@ -50,7 +50,6 @@
 namespace onela {
 namespace {
 
-constexpr uint64_t kWaitNs = 2000000000ull;  // bound of every wait
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 256;  // scores behind the outputs in tensor memory
 constexpr int TT = 64;           // tokens per tile
@@ -95,9 +94,11 @@ __device__ __forceinline__ void cp_wait() {
 }
 // Wait of a whole warp, which goes on together and alike: `dead` is the same in
 // all its lanes (a barrier may complete between two lanes' last looks at it).
-// No wait once one has run out.
-__device__ __forceinline__ void wait_warp(uint64_t *bar, uint32_t parity, bool &dead) {
-  if (!dead && !ptx::mbar_wait(bar, parity, kWaitNs)) dead = true;
+// No wait once one has run out.  A warp whose wait ran out hands nothing on from
+// then: it issues no copy and no product and arrives on no barrier of the
+// others, whose own waits then run out too before they take anything unfinished.
+__device__ __forceinline__ void wait_warp(const AttnParams &p, uint64_t *bar, uint32_t parity, bool &dead) {
+  if (!dead && !ptx::mbar_wait(bar, parity, p.wait_ns)) dead = true;
   dead = __any_sync(0xffffffffu, dead);
 }
 
@@ -117,14 +118,15 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
 
   constexpr int kMmaWarp = C::kSoft / 32 + 4;
   if (tid == 0) {
+    // stall (tests): an arrival that never comes.
     for (int i = 0; i < 4; ++i) {
-      ptx::mbar_init(&sh.kfull[i], 4);
-      ptx::mbar_init(&sh.vfull[i], 4);
-      ptx::mbar_init(&sh.kempty[i], 1);
-      ptx::mbar_init(&sh.vempty[i], 1);
-      ptx::mbar_init(&sh.s[i], 1);
-      ptx::mbar_init(&sh.p[i], 128);
-      ptx::mbar_init(&sh.pv[i], 1);
+      ptx::mbar_init(&sh.kfull[i], 4 + (p.stall == kStallFull));
+      ptx::mbar_init(&sh.vfull[i], 4 + (p.stall == kStallFull));
+      ptx::mbar_init(&sh.kempty[i], 1 + (p.stall == kStallEmpty));
+      ptx::mbar_init(&sh.vempty[i], 1 + (p.stall == kStallEmpty));
+      ptx::mbar_init(&sh.s[i], 1 + (p.stall == kStallScores));
+      ptx::mbar_init(&sh.p[i], 128 + (p.stall == kStallWeights));
+      ptx::mbar_init(&sh.pv[i], 1 + (p.stall == kStallOutputs));
     }
     ptx::mbar_init(&sh.q, C::kSoft);
     ptx::mbar_init(&sh.done[0], 1);
@@ -168,7 +170,7 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
         // By boxes of 64 rows, or a warp brings its 32 rows, 32 16-byte chunks at a time.
         uint8_t *qd = smem + (kSub == 2 ? grp * C::kQ : 0);
         if (maps.q_box) {
-          if (warp == 4 * grp && lane == 0) {
+          if (warp == 4 * grp && lane == 0 && !dead) {
             ptx::fence_proxy_async();  // the rows that went out through this memory were written by plain stores
             ptx::mbar_expect_tx(&sh.q, C::kQ);
 #pragma unroll
@@ -191,7 +193,7 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
         }
       }
       ptx::fence_proxy_async();
-      ptx::mbar_arrive(&sh.q);
+      if (!dead) ptx::mbar_arrive(&sh.q);
 
       float mref = -CUDART_INF_F, sum = 0.f;
       bool any = false;  // this group has a product in O
@@ -199,7 +201,7 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
       for (int t = kSub == 1 ? grp : 0; t < nt; t += kStep, ++c) {
         const int b = grp * 2 + (c & 1);
         const uint32_t s_t = tmem + lanes + kSCol + b * TT;
-        wait_warp(&sh.s[b], (c >> 1) & 1, dead);
+        wait_warp(p, &sh.s[b], (c >> 1) & 1, dead);
         ptx::tc_fence_after();
         float x[2][32];
         ptx::tmem_ld32(s_t, x[0]);
@@ -223,7 +225,7 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
           const float f = grow ? exp2_sub(mref, top) : 1.f;
           if (any) {
             // The group's last product into O must be done.
-            wait_warp(&sh.pv[b ^ 1], ((c - 1) >> 1) & 1, dead);
+            wait_warp(p, &sh.pv[b ^ 1], ((c - 1) >> 1) & 1, dead);
             ptx::tc_fence_after();
 #pragma unroll 1
             for (int e = 0; e < D / 16; ++e) {
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
         }
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
-        ptx::mbar_arrive(&sh.p[b]);
+        if (!dead) ptx::mbar_arrive(&sh.p[b]);
         const float2 sw = un((s4[0] + s4[1]) + (s4[2] + s4[3]));
         sum += sw.x + sw.y;
       }
@@ -269,7 +271,7 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
       const int slot = G == 2 && kSub == 1 ? 2 * walk.slot + grp : walk.slot;
       const int64_t pr = part_row(p, slot, h, m);
       if (any) {
-        wait_warp(&sh.pv[grp * 2 + ((c - 1) & 1)], ((c - 1) >> 1) & 1, dead);
+        wait_warp(p, &sh.pv[grp * 2 + ((c - 1) & 1)], ((c - 1) >> 1) & 1, dead);
         ptx::tc_fence_after();
       }
       // Rows go out 128 bytes at a time: 32 columns of the warp's 32 rows through shared memory.
@@ -321,7 +323,7 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
         if (lane == 0) ptx::mbar_arrive(full_bar(i));
       });
     };
-    while (walk.next(p)) {
+    while (!dead && walk.next(p)) {
       const int32_t *tab = p.table + (int64_t)walk.r * p.row_pages;
       const int nt = (walk.hi - walk.lo + TT - 1) / TT;
       // Where this warp's 16 tokens of a tile are: page * Hkv + head (-1: not
@@ -340,7 +342,7 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
       };
       const int first = walk.lo + lw * kTokW;
       if (!one_page) entry(lane < kTokW ? first + lane : walk.hi);
-      for (int t = 0; t < nt; ++t) {
+      for (int t = 0; t < nt && !dead; ++t) {
         int cph = ph, cplace = place;
         if (one_page) {
           if (t % 32 == 0) entry(first + (t + lane) * TT);
@@ -362,8 +364,9 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
               cp_wait<0>();
               tell(it);
             }
-            wait_warp(empty, (n - 1) & 1, dead);
+            wait_warp(p, empty, (n - 1) & 1, dead);
           }
+          if (dead) break;
           if (kv == 0 && lane == 0) sh.mask[(it >> 1) & 7][lw] = here;
           uint8_t *dst = smem + (kv ? C::oV : C::oK) + st * C::kTile;
           if (boxes) {
@@ -401,10 +404,13 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
     cp_wait<0>();
     tell(it);
     // Boxes of a piece that was given up may still be on their way: no CTA
-    // ends before its copies have landed.
+    // ends before its copies have landed (they have, too, once a wait has run out).
     for (uint32_t i = it < 2 * NS ? 0 : it - 2 * NS; i < it; ++i) {
       const uint32_t turn = (i >> 1) / NS;
-      if (!ptx::mbar_wait(full_bar(i), turn & 1, kWaitNs)) dead = true;
+      if (!ptx::mbar_wait(full_bar(i), turn & 1, p.wait_ns)) {
+        dead = true;
+        break;
+      }
     }
   } else {
     // ----------------------------------------------------------- products
@@ -425,7 +431,7 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
       // Jobs in the order of issue: job j of the piece is group j % G's, tile
       // j (kSub = 1) or j / 2 (kSub = 2).
       const int nj = nt * kSub;
-      if (is_s) wait_warp(&sh.q, nq & 1, dead);
+      if (is_s) wait_warp(p, &sh.q, nq & 1, dead);
       ++nq;
       for (int j0 = 0; j0 < nj; j0 += G) {
 #pragma unroll
@@ -437,9 +443,9 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
           const uint32_t st = tiles % NS, turn = tiles / NS;
           if (last) ++tiles;
           if (is_s) {
-            if (first) wait_warp(&sh.kfull[st], turn & 1, dead);
+            if (first) wait_warp(p, &sh.kfull[st], turn & 1, dead);
             // The weights that were in this buffer have been used.
-            if (cg >= 2) wait_warp(&sh.pv[b], ((cg >> 1) - 1) & 1, dead);
+            if (cg >= 2) wait_warp(p, &sh.pv[b], ((cg >> 1) - 1) & 1, dead);
             ptx::tc_fence_after();
             const uint64_t qa = qd + (kSub == 2 ? g * (C::kQ >> 4) : 0), ka = kd + st * (C::kTile >> 4);
             const uint32_t to = tmem + kSCol + b * TT;
@@ -452,8 +458,8 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
               if (last) ptx::mma_commit(&sh.kempty[st]);
             }
           } else {
-            if (first) wait_warp(&sh.vfull[st], turn & 1, dead);
-            wait_warp(&sh.p[b], (cg >> 1) & 1, dead);
+            if (first) wait_warp(p, &sh.vfull[st], turn & 1, dead);
+            wait_warp(p, &sh.p[b], (cg >> 1) & 1, dead);
             ptx::tc_fence_after();
             const uint64_t va = vd + st * (C::kTile >> 4);
             const uint32_t to = tmem + (G == 2 ? g * 128 : 0), from = tmem + kSCol + b * TT;
@@ -471,8 +477,8 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
     }
     if (nq > 0) {
       if (ptx::elect_one()) ptx::mma_commit(&sh.done[is_s]);
-      if (!ptx::mbar_wait(&sh.done[is_s], 0, kWaitNs)) dead = true;
-      if (is_s && !ptx::mbar_wait(&sh.q, (nq - 1) & 1, kWaitNs)) dead = true;  // Q's boxes have landed
+      if (!ptx::mbar_wait(&sh.done[is_s], 0, p.wait_ns)) dead = true;
+      if (is_s && !ptx::mbar_wait(&sh.q, (nq - 1) & 1, p.wait_ns)) dead = true;  // Q's boxes have landed
     }
   }
   if (dead) set_status(p.status, ONELA_STATUS_TIMEOUT);
@@ -531,10 +537,11 @@ __global__ void __launch_bounds__(MassCfg<D>::kThreads, D == 256 ? 1 : 2) attn_m
   if (tid == 0) {
     ptx::mbar_init(&sh.k, 128);
     for (int i = 0; i < 4; ++i) {
-      ptx::mbar_init(&sh.full[i], 128);
-      ptx::mbar_init(&sh.empty[i], 128);  // by the threads that took the stage's tile: its product is done by then
-      ptx::mbar_init(&sh.s[i], 1);
-      ptx::mbar_init(&sh.sfree[i], 128);
+      ptx::mbar_init(&sh.full[i], 128 + (p.stall == kStallMassFull));
+      // By the threads that took the stage's tile: its product is done by then.
+      ptx::mbar_init(&sh.empty[i], 128 + (p.stall == kStallMassEmpty));
+      ptx::mbar_init(&sh.s[i], 1 + (p.stall == kStallMassScores));
+      ptx::mbar_init(&sh.sfree[i], 128 + (p.stall == kStallMassRead));
     }
     ptx::mbar_init(&sh.done, 1);
     ptx::mbar_fence_init();
@@ -557,7 +564,7 @@ __global__ void __launch_bounds__(MassCfg<D>::kThreads, D == 256 ? 1 : 2) attn_m
     uint32_t c = 0;
     for (int t = grp; t < nt; t += 2, ++c) {
       const int b = grp * 2 + (c & 1), st = t % NS;
-      wait_warp(&sh.s[b], (c >> 1) & 1, dead);
+      wait_warp(p, &sh.s[b], (c >> 1) & 1, dead);
       ptx::tc_fence_after();
       float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -570,10 +577,12 @@ __global__ void __launch_bounds__(MassCfg<D>::kThreads, D == 256 ? 1 : 2) attn_m
       }
       sum += (a[0] + a[1]) + (a[2] + a[3]);
       ptx::tc_fence_before();
-      ptx::mbar_arrive(&sh.sfree[b]);
-      ptx::mbar_arrive(&sh.empty[st]);
+      if (!dead) {
+        ptx::mbar_arrive(&sh.sfree[b]);
+        ptx::mbar_arrive(&sh.empty[st]);
+      }
     }
-    if (grp == 1) sh.sums[tok] = sum;
+    if (grp == 1) sh.sums[tok] = dead ? CUDART_NAN_F : sum;
     ptx::bar_sync(1, 256);
     if (grp == 0 && t0 + tok < len) {
       const int64_t at = (int64_t)rh * p.cap + t0 + tok;
@@ -620,9 +629,12 @@ __global__ void __launch_bounds__(MassCfg<D>::kThreads, D == 256 ? 1 : 2) attn_m
       ptx::fence_proxy_async();
       ptx::mbar_arrive(&sh.full[t % NS]);
     };
+    int issued = 0;  // tiles; all of them, unless a wait ran out
     for (int t = 0; t < nt; ++t) {
       const int st = t % NS;
-      if (t >= NS) wait_warp(&sh.empty[st], (t / NS - 1) & 1, dead);
+      if (t >= NS) wait_warp(p, &sh.empty[st], (t / NS - 1) & 1, dead);
+      if (dead) break;
+      issued = t + 1;
       uint8_t *dst = smem + C::kK + st * C::kTile;
       const int m = t * 64 + lw * 16 + lane;  // lanes 0 .. 15: this warp's rows
       const int64_t mine = lane < 16 && m < p.M
@@ -662,20 +674,23 @@ __global__ void __launch_bounds__(MassCfg<D>::kThreads, D == 256 ? 1 : 2) attn_m
       }
     }
     cp_wait<0>();
-    tell(nt - 1);
+    tell(issued - 1);
     // No CTA ends before its boxes have landed.
-    if (!ptx::mbar_wait(&sh.k, 0, kWaitNs)) dead = true;
-    for (int t = max(0, nt - NS); t < nt; ++t)
-      if (!ptx::mbar_wait(&sh.full[t % NS], (t / NS) & 1, kWaitNs)) dead = true;
+    if (!ptx::mbar_wait(&sh.k, 0, p.wait_ns)) dead = true;
+    for (int t = max(0, issued - NS); t < issued; ++t)
+      if (!ptx::mbar_wait(&sh.full[t % NS], (t / NS) & 1, p.wait_ns)) {
+        dead = true;
+        break;
+      }
   } else {
     // ----------------------------------------------------------- products
     constexpr uint32_t id = ptx::idesc_bf16_f32(128, 64);
     const uint64_t kd = ptx::desc_k128(base), qd = ptx::desc_k128(base + C::kK);
-    wait_warp(&sh.k, 0, dead);
+    wait_warp(p, &sh.k, 0, dead);
     for (int t = 0; t < nt; ++t) {
       const int g = t & 1, n = t >> 1, b = g * 2 + (n & 1), st = t % NS;
-      wait_warp(&sh.full[st], (t / NS) & 1, dead);
-      if (n >= 2) wait_warp(&sh.sfree[b], ((n >> 1) - 1) & 1, dead);
+      wait_warp(p, &sh.full[st], (t / NS) & 1, dead);
+      if (n >= 2) wait_warp(p, &sh.sfree[b], ((n >> 1) - 1) & 1, dead);
       ptx::tc_fence_after();
       const uint64_t qa = qd + st * (C::kTile >> 4);
       if (!dead && ptx::elect_one()) {
@@ -688,7 +703,7 @@ __global__ void __launch_bounds__(MassCfg<D>::kThreads, D == 256 ? 1 : 2) attn_m
       __syncwarp();
     }
     if (ptx::elect_one()) ptx::mma_commit(&sh.done);
-    if (!ptx::mbar_wait(&sh.done, 0, kWaitNs)) dead = true;
+    if (!ptx::mbar_wait(&sh.done, 0, p.wait_ns)) dead = true;
   }
   if (dead) set_status(p.status, ONELA_STATUS_TIMEOUT);
   __syncwarp();

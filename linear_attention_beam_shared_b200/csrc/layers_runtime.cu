@@ -1,6 +1,6 @@
 // Entry points of the operators around a GDN layer (include/onela.h): checks
 // of the arguments on the host, then the launches.  Nothing is kept between
-// calls but their number, and nothing is allocated.
+// calls but their number and the wait policy, and nothing is allocated.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -21,6 +21,8 @@ cudaError_t launch_attention(const onela_attention_config &c, AttnParams &p, voi
 namespace {
 
 std::atomic<uint64_t> g_calls{0};
+std::atomic<uint64_t> g_wait_ns{2000000000};  // onela_set_attention_wait_policy
+std::atomic<int> g_stall{0};
 
 bool valid_dtype(int d) { return d == ONELA_F32 || d == ONELA_BF16; }
 size_t esize(int d) { return d == ONELA_BF16 ? 2 : 4; }
@@ -135,12 +137,22 @@ int onela_paged_attention(const onela_attention_config *cfg, const void *q, cons
   p.o = o;
   p.lse = lse;
   p.status = status;
+  p.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+  p.stall = g_stall.load(std::memory_order_relaxed);
   if (c.kernel == ONELA_KERNEL_TC && !onela::attention_tc_supports(c, p)) return ONELA_ERR_UNSUPPORTED;
   const size_t need = onela::attention_scratch_bytes(c, mass_out != nullptr, p);
   if (need > 0 && (!scratch || !aligned(scratch, 256))) return ONELA_ERR_ARG;
   if (scratch_bytes < need) return ONELA_ERR_SCRATCH;
   return on_device(c.device,
                    [&] { return onela::launch_attention(c, p, scratch, static_cast<cudaStream_t>(stream)); });
+}
+
+int onela_set_attention_wait_policy(uint64_t limit_ns, int32_t stall) {
+  if (limit_ns < 1000000ull || limit_ns > 10000000000ull || stall < 0 || stall >= onela::kStallEnd)
+    return ONELA_ERR_ARG;
+  g_wait_ns.store(limit_ns, std::memory_order_relaxed);
+  g_stall.store(stall, std::memory_order_relaxed);
+  return ONELA_OK;
 }
 
 int onela_cache_write(const onela_cache_write_config *cfg, const void *k, const void *v, void *k_pool, void *v_pool,

@@ -198,3 +198,13 @@ def test_binding_refuses_sizes_that_do_not_fit_their_fields():
         bad[i] += 2 ** 32
         with pytest.raises(ValueError):
             _layers._config(("test", tuple(bad)), _layers.onela_cache_evict_config, bad, None)
+
+
+def test_attention_wait_policy_refuses_bad_bounds():
+    import linear_attention_beam_shared_b200 as L
+    f = L._lib.lib.onela_set_attention_wait_policy
+    for limit, stall in ((999_999, 0), (10**10 + 1, 0), (10**9, -1), (10**9, 10)):
+        assert f(limit, stall) == L.ONELA_ERR_ARG
+        with pytest.raises(L.OnelaError):
+            L.onela_set_attention_wait_policy(limit, stall)
+    assert f(2_000_000_000, 0) == 0
