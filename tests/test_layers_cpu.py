@@ -208,3 +208,18 @@ def test_attention_wait_policy_refuses_bad_bounds():
         with pytest.raises(L.OnelaError):
             L.onela_set_attention_wait_policy(limit, stall)
     assert f(2_000_000_000, 0) == 0
+
+
+def test_scratch_bytes_of_a_spaced_out_q():
+    """A token stride that rules the tensor-core kernels out needs the general kernel's scratch."""
+    import linear_attention_beam_shared_b200 as L
+    sizes = (2, 64, 8, 2, 64, "bf16", 16, 100, 40)
+    for mass in (False, True):
+        general = L.onela_paged_attention_scratch_bytes(*sizes, want_mass=mass, kernel=L.ONELA_KERNEL_SIMT)
+        dense = L.onela_paged_attention_scratch_bytes(*sizes, want_mass=mass)
+        assert general != dense > 0
+        assert L.onela_paged_attention_scratch_bytes(*sizes, want_mass=mass, q_stride=8 * 64 + 8) == dense
+        assert L.onela_paged_attention_scratch_bytes(*sizes, want_mass=mass, q_stride=8 * 64 + 3) == general
+    assert L.onela_paged_attention_scratch_bytes(*sizes, q_stride=8 * 64 - 1) == 0
+    with pytest.raises(ValueError):
+        L.onela_paged_attention_scratch_bytes(*sizes, q_stride=1 << 63)

@@ -149,3 +149,27 @@ def test_parts_that_cross_requests(lengths, W, H_q, H, d, tiles, pieces):
     k, v, table, shown = build(gen, lengths, H, 16, d, torch.bfloat16)
     q = torch.randn((len(lengths), W, H_q, d), generator=gen, device="cuda").bfloat16()
     check(q, k, v, table, shown, lengths, tiles, pieces)
+
+
+@pytest.mark.parametrize("W,pad", [(1, 3), (40, 3), (40, 8), (40, 1)])
+def test_one_scratch_buffer_for_a_slice_of_a_projection(W, pad):
+    """q as a slice of a projection whose token stride is or is not a multiple
+    of 8: the call takes the buffer that was sized for that stride."""
+    import linear_attention_beam_shared_b200 as L
+    gen = torch.Generator(device="cuda").manual_seed(W + pad)
+    H, G, d, page, n = 2, 4, 64, 16, 700
+    k, v, table, shown = build(gen, [n], H, page, d, torch.bfloat16)
+    stride = H * G * d + pad
+    wide = torch.randn((1, W, stride), generator=gen, device="cuda").bfloat16()
+    q = wide[:, :, :H * G * d].unflatten(-1, (H * G, d))
+    need = L.onela_paged_attention_scratch_bytes(1, W, H * G, H, d, "bf16", page, k.shape[0], table.shape[1], want_mass=True,
+                                                 q_stride=stride)
+    scratch = torch.empty(need, dtype=torch.uint8, device="cuda")
+    lengths = torch.tensor([n], dtype=torch.int32, device="cuda")
+    out = [torch.zeros((1, H, table.shape[1] * page), device="cuda") for _ in range(2)]
+    a = L.onela_paged_attention(q, k, v, table, lengths, mass_out=out[0], scratch=scratch)
+    b = L.onela_paged_attention(q, k, v, table, lengths, mass_out=out[1])
+    assert torch.equal(a, b) and torch.equal(*out)
+    check(q, k, v, table, shown, [n], 11, 11)
+    with pytest.raises(L.OnelaError):
+        L.onela_paged_attention(q, k, v, table, lengths, mass_out=out[0], scratch=scratch[:need - 256])
