@@ -507,7 +507,10 @@ enum {
  *   d                 head width, 1 .. 256.
  *   dtype             ONELA_F32 or ONELA_BF16: of q, the pools and o.
  *                     Products are accumulated and the softmax is taken in
- *                     fp32 either way.
+ *                     fp32 either way, of differences of scores, so their size
+ *                     alone loses nothing.  o is summed before it is divided by
+ *                     the sum of weights, each weight at most 2^8, so |v| times
+ *                     2^8 times the tokens has to stay below 3e38.
  *   kernel            ONELA_KERNEL_AUTO; ONELA_KERNEL_SIMT (any shape) or
  *                     ONELA_KERNEL_TC (bf16, d in {64, 128, 256}, pools and q
  *                     rows on 16-byte boundaries, o on 4) to force one.

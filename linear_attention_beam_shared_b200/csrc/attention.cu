@@ -231,10 +231,10 @@ __global__ void __launch_bounds__(kThreads, 4) attn_simt(AttnParams p) {
 #pragma unroll
       for (int e = 0; e < kOwn; ++e) {
         const int m = m0 + kOwn * warp + e;
-        const float x = (live >> lane) & 1 ? s[e] * p.scale_log2 : -CUDART_INF_F;
+        const float x = (live >> lane) & 1 ? s[e] : -CUDART_INF_F;
         if (p.scores && m < p.M && pos < hi) p.scores[(((int64_t)r * p.Hkv + h) * p.M + m) * p.cap + pos] = x;
         const float mnew = fmaxf(mx[e], warp_max(x));
-        const float w = exp2_sub(x, mnew), f = exp2_sub(mx[e], mnew);
+        const float w = exp2_sub(x, mnew, p.scale_log2), f = exp2_sub(mx[e], mnew, p.scale_log2);
         sum[e] = sum[e] * f + warp_sum(w);
         mx[e] = mnew;
         ps[lane][kOwn * warp + e] = w;
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 4) attn_simt(AttnParams p) {
         const float inv = corr[i] == 0.f ? 0.f : 1.f / corr[i];
         if (c0 < p.d) store_f(o + orow * p.d + c0, acc0[i] * inv);
         if (c1 < p.d) store_f(o + orow * p.d + c1, acc1[i] * inv);
-        if (tid == 0 && p.lse) p.lse[orow] = corr[i] == 0.f ? -CUDART_INF_F : (ps[0][i] + log2f(corr[i])) * kLn2;
+        if (tid == 0 && p.lse) p.lse[orow] = corr[i] == 0.f ? -CUDART_INF_F : (ps[0][i] * p.scale_log2 + log2f(corr[i])) * kLn2;
       }
       continue;
     }
@@ -470,18 +470,18 @@ __global__ void __launch_bounds__(kWpr == 1 ? 128 : kWpr * 32, kWpr == 1 ? (kGr 
             float t = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) t += qv[i] * x[i];
-            t = group_sum(t) * p.scale_log2;
+            t = group_sum(t);
             s[j] = (there >> j) & 1 ? t : -CUDART_INF_F;
             top = fmaxf(top, s[j]);
           }
-          const float f = exp2_sub(mx[g], top);
+          const float f = exp2_sub(mx[g], top, p.scale_log2);
           mx[g] = top;
           sum[g] *= f;
 #pragma unroll
           for (int i = 0; i < 8; ++i) acc[g][i] *= f;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float e = exp2_sub(s[j], top);
+            const float e = exp2_sub(s[j], top, p.scale_log2);
             vv[j].get(x);
             sum[g] += e;
 #pragma unroll
@@ -509,8 +509,8 @@ __global__ void __launch_bounds__(kWpr == 1 ? 128 : kWpr * 32, kWpr == 1 ? (kGr 
 #pragma unroll
       for (int o = kL / 2; o; o >>= 1) mnew = fmaxf(mnew, __shfl_xor_sync(0xffffffffu, mnew, o));
       mnew = fmaxf(mx[g], mnew);
-      const float f = exp2_sub(mx[g], mnew);
-      e[g] = exp2_sub(ml[g].x, mnew);
+      const float f = exp2_sub(mx[g], mnew, p.scale_log2);
+      e[g] = exp2_sub(ml[g].x, mnew, p.scale_log2);
       sum[g] = sum[g] * f + group_sum(ml[g].y * e[g]);
       mx[g] = mnew;
 #pragma unroll
@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(kWpr == 1 ? 128 : kWpr * 32, kWpr == 1 ? (kGr 
     for (int i = 0; i < 8; ++i) acc[0][i] = 0.f;
 #pragma unroll
     for (int j = 0; j < kWpr; ++j) {
-      const float f = exp2_sub(wml[j][grp].x, top);
+      const float f = exp2_sub(wml[j][grp].x, top, p.scale_log2);
       sum[0] += wml[j][grp].y * f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[0][i] += wacc[j][lane + 32 * i] * f;
@@ -563,15 +563,14 @@ __global__ void __launch_bounds__(kWpr == 1 ? 128 : kWpr * 32, kWpr == 1 ? (kGr 
     for (int i = 0; i < 8; ++i) acc[g][i] *= inv;
     C::store(static_cast<T *>(p.o) + orow * p.d, gl, p.d, acc[g]);
     if (gl == 0) {
-      const float l2 = sum[g] == 0.f ? -CUDART_INF_F : mx[g] + log2f(sum[g]);
-      if (p.lse) p.lse[orow] = l2 * kLn2;
-      if (p.lse2) p.lse2[((int64_t)r * p.Hkv + h) * p.M + m + g] = l2;
+      if (p.lse) p.lse[orow] = sum[g] == 0.f ? -CUDART_INF_F : (mx[g] * p.scale_log2 + log2f(sum[g])) * kLn2;
+      if (p.norm) p.norm[((int64_t)r * p.Hkv + h) * p.M + m + g] = make_float2(sum[g] == 0.f ? CUDART_INF_F : mx[g], inv);
     }
   }
 }
 
 // The weight each prompt position drew, from the scores the split kernel
-// stored: sum exp2(s - lse2) over the M rows.  A thread takes four positions
+// stored: sum exp2(s - max) / sum over the M rows.  A thread takes four positions
 // (kP; one where rows are no multiple of 4) and, for few rows, all of these;
 // for many the CTA's four warps take every fourth row each of the same positions
 // (kSplit = 4), joined through shared memory in a fixed order.
@@ -587,7 +586,8 @@ __global__ void __launch_bounds__(kThreads) attn_mass(const __grid_constant__ At
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
   if (first >= len) return;
-  const float *l2 = p.lse2 + (int64_t)rh * p.M, *sc = p.scores + (int64_t)rh * p.M * p.cap + pos;
+  const float2 *norm = p.norm + (int64_t)rh * p.M;
+  const float *sc = p.scores + (int64_t)rh * p.M * p.cap + pos;
   float t[kP];
 #pragma unroll
   for (int i = 0; i < kP; ++i) t[i] = 0.f;
@@ -596,9 +596,9 @@ __global__ void __launch_bounds__(kThreads) attn_mass(const __grid_constant__ At
     for (int m = warp; m < p.M; m += kSplit) {
       float x[kP];
       ldn<kP, true>(sc + (int64_t)m * p.cap, x);
-      const float l = l2[m];
+      const float2 l = norm[m];
 #pragma unroll
-      for (int i = 0; i < kP; ++i) t[i] += exp2_sub(x[i], l);
+      for (int i = 0; i < kP; ++i) t[i] += exp2_sub(x[i], l.x, p.scale_log2) * l.y;
     }
   }
   if constexpr (kSplit > 1) {
@@ -707,7 +707,7 @@ size_t plan_call(const onela_attention_config &c, bool want_mass, AttnParams &p,
     p.part_ml = reinterpret_cast<float2 *>(take(rows * 8));
   }
   if (want_mass) {
-    p.lse2 = reinterpret_cast<float *>(take((size_t)p.R * p.Hkv * p.M * 4));
+    p.norm = reinterpret_cast<float2 *>(take((size_t)p.R * p.Hkv * p.M * 8));
     if (kind != kAttnWide) p.scores = reinterpret_cast<float *>(take((size_t)p.R * p.Hkv * p.M * p.cap * 4));
   }
   used = kind;

@@ -15,8 +15,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // One call.  A (request, key-value head) has M = W * G query rows, row m
-// being head m % G of the group of beam m / G.  Scores are kept times log2(e)
-// so that the softmax is taken with exp2.
+// being head m % G of the group of beam m / G.  Scores and their maxima are kept
+// as the products q.k come out; a weight is exp2((score - maximum) * scale *
+// log2(e)).  The difference comes first: equal scores are equal to the maximum
+// exactly, however large they are, and the rounded argument is off by a part of
+// the difference, not of the score.
 struct AttnParams {
   int R, W, Hq, Hkv, d, G, M;
   int page, pages, row_pages;
@@ -40,10 +43,13 @@ struct AttnParams {
   int per_slot;         // results per slot (two where two warp groups share the rows)
   int direct;           // a CTA per request and no beam segment: the split kernel writes o itself
   // Scratch: per (slot, key-value head, row) the unnormalised output and
-  // (maximum, sum); lse2 [R][Hkv][M] and scores [R][Hkv][M][cap] for the mass.
+  // (maximum, sum); for the mass norm [R][Hkv][M], a row's (maximum, 1 / sum),
+  // +inf and 0 where it has nothing to attend to (not its lse: next to a large
+  // maximum the logarithm of the sum would lose its bits, and weights with it),
+  // and scores [R][Hkv][M][cap].
   float *part_o;
   float2 *part_ml;
-  float *lse2;
+  float2 *norm;
   float *scores;
   // Of the tensor-core kernel's waits between its warps: the bound of each, and
   // (tests) the barriers that expect one arrival more than will come.
@@ -256,14 +262,22 @@ __device__ __forceinline__ float warp_sum(float x) {
   for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
-// exp2(a - b), b >= a: 0 for a = -inf, even where b is -inf too (nothing seen
-// yet); NaN stays NaN.
-__device__ __forceinline__ float exp2_sub(float a, float b) { return a == -CUDART_INF_F ? 0.f : exp2f(a - b); }
+// exp2((a - b) * scale), b >= a: 0 for a = -inf, even where b is -inf too (nothing
+// seen yet); NaN stays NaN.
+__device__ __forceinline__ float exp2_sub(float a, float b, float scale) {
+  return a == -CUDART_INF_F ? 0.f : exp2f((a - b) * scale);
+}
 
 // 2^x by the special-function unit (2 ulp); results below 2^-126 become 0.
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The smaller of two; NaN if either is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {

@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) attn_narrow(const __g
           for (int e = 0; e < 4; ++e) {
             const int m = 8 * nt + 2 * t4 + (e & 1), pos = at + 8 * (e >> 1);
             if (m < p.M && pos < hi)
-              p.scores[(((int64_t)r * p.Hkv + h) * p.M + m) * p.cap + pos] = s[nt][e] * p.scale_log2;
+              p.scores[(((int64_t)r * p.Hkv + h) * p.M + m) * p.cap + pos] = s[nt][e];
           }
       }
       // The rows' maxima over the tile, of all lanes with the same t4.
@@ -237,18 +237,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) attn_narrow(const __g
       for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float t = fmaxf(s[nt][e], s[nt][e + 2]) * p.scale_log2;
+          float t = fmaxf(s[nt][e], s[nt][e + 2]);
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
           top[nt][e] = t;
-          grow = grow || t > mref[nt][e] + kSlack || (mref[nt][e] == -CUDART_INF_F && t > mref[nt][e]);
+          grow = grow || (t - mref[nt][e]) * p.scale_log2 > kSlack;  // from -inf: always, unless there is nothing yet
         }
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float mnew = fmaxf(mref[nt][e], top[nt][e]), f = exp2_sub(mref[nt][e], mnew);
+            const float mnew = fmaxf(mref[nt][e], top[nt][e]), f = exp2_sub(mref[nt][e], mnew, p.scale_log2);
             mref[nt][e] = mnew;
             sum[nt][e] *= f;
 #pragma unroll
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) attn_narrow(const __g
         const float o1 = mref[nt][1] == -CUDART_INF_F ? 0.f : mref[nt][1];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const float a = ex2(fmaf(s[nt][2 * t], p.scale_log2, -o0)), b = ex2(fmaf(s[nt][2 * t + 1], p.scale_log2, -o1));
+          const float a = ex2((s[nt][2 * t] - o0) * p.scale_log2), b = ex2((s[nt][2 * t + 1] - o1) * p.scale_log2);
           sum[nt][0] += a;
           sum[nt][1] += b;
           const uint32_t hi2 = pack_bf16(a, b);
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) attn_narrow(const __g
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float f = exp2_sub(ml[w].x, top);
+        const float f = exp2_sub(ml[w].x, top, p.scale_log2);
         const float4 x = *reinterpret_cast<const float4 *>(all + (w * 8 * kNT + m) * kLd + c);
         l += ml[w].y * f;
         o.x += x.x * f;
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) attn_narrow(const __g
         __nv_bfloat162 *out = reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(p.o) + orow * D + c);
         out[0] = __floats2bfloat162_rn(o.x * inv, o.y * inv);
         out[1] = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-        if (c == 0 && p.lse) p.lse[orow] = l == 0.f ? -CUDART_INF_F : (top + log2f(l)) * kLn2;
+        if (c == 0 && p.lse) p.lse[orow] = l == 0.f ? -CUDART_INF_F : (top * p.scale_log2 + log2f(l)) * kLn2;
       } else {
         const int64_t pr = part_row(p, walk.slot, h, m);
         *reinterpret_cast<float4 *>(p.part_o + pr * D + c) = o;

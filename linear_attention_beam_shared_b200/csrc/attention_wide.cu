@@ -218,11 +218,12 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
         float t4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
         for (int i = 0; i < 64; ++i) t4[i & 3] = fmaxf(t4[i & 3], x[i >> 5][i & 31]);
-        const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * p.scale_log2;
-        // Move the reference when the maximum outgrew it (or on the first tile).
-        const bool grow = top > mref + kSlack || (mref == -CUDART_INF_F && top > mref);
+        const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+        // Move the reference when the maximum outgrew it (from -inf: always,
+        // unless there is nothing yet).
+        const bool grow = (top - mref) * p.scale_log2 > kSlack;
         if (__any_sync(0xffffffffu, grow)) {
-          const float f = grow ? exp2_sub(mref, top) : 1.f;
+          const float f = grow ? exp2_sub(mref, top, p.scale_log2) : 1.f;
           if (any) {
             // The group's last product into O must be done.
             wait_warp(p, &sh.pv[b ^ 1], ((c - 1) >> 1) & 1, dead);
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
           uint32_t y[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float2 w = un(fma2(f2(x[e >> 1][(e & 1) * 16 + 2 * i], x[e >> 1][(e & 1) * 16 + 2 * i + 1]), sc2, off2));
+            const float2 w = un((f2(x[e >> 1][(e & 1) * 16 + 2 * i], x[e >> 1][(e & 1) * 16 + 2 * i + 1]) + off2) * sc2);
             const float a = ex2(w.x), bb = ex2(w.y);
             s4[i & 3] = s4[i & 3] + f2(a, bb);
             y[i] = pack_bf16(a, bb);
@@ -492,9 +493,9 @@ __global__ void __launch_bounds__(Cfg<D, kSub>::kThreads, 1) attn_wide(const __g
 }
 
 // ---------------------------------------------------------------------------
-// The weight each prompt position drew, once every row's lse is known: the
+// The weight each prompt position drew, once every row's (maximum, 1 / sum) is known: the
 // scores again, this time transposed, S^T = K Q^T, so that a thread owns a
-// token and adds exp2(s - lse2) over the rows in order (no atomics, one writer
+// token and adds exp2(s - max) / sum over the rows in order (no atomics, one writer
 // per position).  Recomputing costs half of the attention's products; keeping
 // the scores would cost 4 bytes a row and token, more than K and V themselves
 // from 64 rows on at d = 64.  One CTA per (request, head, 128 tokens): K is an operand
@@ -511,7 +512,7 @@ struct MassCfg {
 struct MassShared {
   uint64_t k, full[4], empty[4], s[4], sfree[4], done;
   uint32_t tmem;
-  alignas(16) float lse2[4][64];  // by Q stage
+  alignas(16) float neg[4][64], inv[4][64];  // of the rows, by Q stage: -maximum, 1 / sum
   float sums[128];
 };
 
@@ -566,16 +567,29 @@ __global__ void __launch_bounds__(MassCfg<D>::kThreads, D == 256 ? 1 : 2) attn_m
       const int b = grp * 2 + (c & 1), st = t % NS;
       wait_warp(p, &sh.s[b], (c >> 1) & 1, dead);
       ptx::tc_fence_after();
-      float a[4] = {0.f, 0.f, 0.f, 0.f};
+      F2 a[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+      const F2 sc2 = f2(p.scale_log2, p.scale_log2);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float x[32];
         ptx::tmem_ld32(tmem + lanes + b * 64 + e * 32, x);
         ptx::tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) a[i & 3] += ex2(fmaf(x[i], p.scale_log2, -sh.lse2[st][e * 32 + i]));
+        for (int i = 0; i < 32; i += 4) {
+          const float4 m = *reinterpret_cast<const float4 *>(&sh.neg[st][e * 32 + i]);
+          const float4 l = *reinterpret_cast<const float4 *>(&sh.inv[st][e * 32 + i]);
+          const float2 w0 = un((f2(x[i], x[i + 1]) + f2(m.x, m.y)) * sc2);
+          const float2 w1 = un((f2(x[i + 2], x[i + 3]) + f2(m.z, m.w)) * sc2);
+          // The maximum is a reference, which scores pass by up to kSlack; the bound
+          // is for scores so large that their last bits, which may come out another
+          // way in this product, are many powers of two.
+          constexpr float kTop = 2.f * kSlack;
+          a[0] = fma2(f2(ex2(min_nan(w0.x, kTop)), ex2(min_nan(w0.y, kTop))), f2(l.x, l.y), a[0]);
+          a[1] = fma2(f2(ex2(min_nan(w1.x, kTop)), ex2(min_nan(w1.y, kTop))), f2(l.z, l.w), a[1]);
+        }
       }
-      sum += (a[0] + a[1]) + (a[2] + a[3]);
+      const float2 at2 = un(a[0] + a[1]);
+      sum += at2.x + at2.y;
       ptx::tc_fence_before();
       if (!dead) {
         ptx::mbar_arrive(&sh.sfree[b]);
@@ -656,12 +670,13 @@ __global__ void __launch_bounds__(MassCfg<D>::kThreads, D == 256 ? 1 : 2) attn_m
                         static_cast<const uint8_t *>(p.q) + (at < 0 ? 0 : at + cc * 16), at < 0 ? 0 : 16);
       }
       ptx::cp_async_commit();
-      if (t == 0) ptx::pdl_wait();  // the lse of every row is the join's
+      if (t == 0) ptx::pdl_wait();  // the rows' norms are the join's
       if (lt < 64) {
-        // A row that is not there, or drew nothing, adds exp2(-inf) = 0.
+        // A row that is not there adds exp2(-inf) = 0, as one that attends to nothing.
         const int mm = t * 64 + lt;
-        const float l = mm < p.M ? p.lse2[(int64_t)rh * p.M + mm] : -CUDART_INF_F;
-        sh.lse2[st][lt] = l == -CUDART_INF_F ? CUDART_INF_F : l;
+        const float2 l = mm < p.M ? p.norm[(int64_t)rh * p.M + mm] : make_float2(CUDART_INF_F, 0.f);
+        sh.neg[st][lt] = -l.x;
+        sh.inv[st][lt] = l.y;
       }
       if (t == 0) {
         cp_wait<1>();

@@ -173,3 +173,45 @@ def test_one_scratch_buffer_for_a_slice_of_a_projection(W, pad):
     check(q, k, v, table, shown, [n], 11, 11)
     with pytest.raises(L.OnelaError):
         L.onela_paged_attention(q, k, v, table, lengths, mass_out=out[0], scratch=scratch[:need - 256])
+
+
+@pytest.mark.parametrize("times", [1.0, 1.7109375, 1.3046875])
+@pytest.mark.parametrize("power", [20, 34, 60, 100])
+@pytest.mark.parametrize("kind", ["all_low", "first_low", "one_high"])
+@pytest.mark.parametrize("W,d,kernel", [(1, 64, 0), (3, 128, 0), (1, 256, 0), (40, 64, 0), (90, 128, 0), (40, 256, 0), (5, 64, 1)])
+def test_scores_far_from_zero(W, d, kernel, kind, power, times):
+    """Scores of 2^power and more, as a fill for tokens that are not to count
+    gives them: the softmax is of differences, so the scores' size alone loses
+    nothing.  q and K are signs times one number, every product q k is exact and
+    equal ones are equal (with `times` the scaled score is not exact), so the weights are those of a few cases: one over the
+    number of tokens that share the largest score, 0 elsewhere (2^-28000 and less)."""
+    import linear_attention_beam_shared_b200 as L
+    H, G, page, n = 2, 4, 16, 64 * 9 + 21
+    gen = torch.Generator(device="cuda").manual_seed(W + d)
+    k, v, table, _ = build(gen, [n], H, page, d, torch.bfloat16)
+    u = torch.sign(torch.randn((H, d), generator=gen, device="cuda"))
+    q = u[None, None, :, None].expand(1, W, H, G, d).reshape(1, W, H * G, d).bfloat16().contiguous()
+    j = torch.arange(n, device="cuda")
+    size = torch.zeros(n, device="cuda")
+    if kind == "all_low":
+        size[:] = -times * 2.0 ** power
+    elif kind == "first_low":
+        size[:200] = -times * 2.0 ** power
+    else:
+        size[311] = times * 2.0 ** power
+    k[table[0].long()[j // page], :, j % page] = (size[:, None, None] * u).bfloat16()
+    top = size == size.max()
+    m = int(top.sum())
+    vv = v[table[0].long()[j // page], :, j % page].double()[top].mean(0)           # [H][d]
+    spread = v[table[0].long()[j // page], :, j % page].double()[top].abs().mean(0)
+    lengths = torch.tensor([n], dtype=torch.int32, device="cuda")
+    mass_out = torch.full((1, H, table.shape[1] * page), -3.0, device="cuda")
+    lse = torch.empty((1, W, H * G), device="cuda")
+    o = L.onela_paged_attention(q, k, v, table, lengths, lse=lse, mass_out=mass_out, kernel=kernel)
+    ref = vv[None, None, :, None].expand(1, W, H, G, d).reshape(o.shape)
+    lim = 2.0 ** -8 * ref.abs() + ((2.0 ** -8 + 200 * U) * spread)[None, None, :, None].expand(1, W, H, G, d).reshape(o.shape)
+    assert bool(((o.double() - ref).abs() <= 1.01 * lim).all())
+    s = float(size.max()) * d * d ** -0.5 + float(torch.tensor(float(m)).log())
+    assert bool(((lse.double() - s).abs() <= abs(s) * 2.0 ** -22 + 1e-5).all())
+    want = torch.where(top, torch.full((n,), W * G / m, device="cuda", dtype=torch.float64), torch.zeros(n, device="cuda", dtype=torch.float64))
+    assert bool(((mass_out[0, :, :n].double() - want).abs() <= want * (200 + W * G) * U + 1e-30).all())
