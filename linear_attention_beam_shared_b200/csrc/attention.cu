@@ -94,10 +94,12 @@ struct SimtLayout {
 // 2).  Per step each warp forms one or two rows' scores (lane = token: a K
 // chunk from shared memory serves both rows, 8 FMAs for 3 loads), takes their
 // softmax by shuffles, and each thread adds to one or two columns of the
-// outputs (one V element for all rows).  Reading the cache bounds it up to
-// four rows (fp32, 32 requests x 16 / 4 heads of 128 on 5120 tokens: 176 us,
-// 3.8 TB/s; latency of the steps and their two barriers keeps it from more),
-// the FMAs beyond.
+// outputs (one V element for all rows).  Up to four rows the latency of the steps
+// and their two block barriers bounds it, well before reading the cache would (32
+// requests x 16 / 4 heads on 5120 tokens, fp32: d = 64 112 us, 128 172 us = 3.9 TB/s,
+// 256, one CTA an SM, 424 us; bf16: d = 96 136 us, 37 by plain loads 252 us), the
+// FMAs beyond: rows past 8 read K and V again (1 request of 256 beams, 16 / 4 heads
+// of 128, 5120 tokens: 839 us in fp32, 748 in bf16).
 template <typename T, int kUnit, int kRows>
 __global__ void __launch_bounds__(kThreads, 4) attn_simt(AttnParams p) {
   extern __shared__ __align__(16) float smem[];

@@ -28,8 +28,8 @@
 // rounding of o itself); its sum is that of the unrounded weights, in fp32.
 //
 // 256 beams of 16 / 4 heads of 128 take 23 us on 5120 tokens (7 of their own
-// each), two thirds of it start, partial outputs and their join, and 89 us on
-// 40960 (961 TFLOP/s; 1150 in steady state, where the scores' products, held by
+// each), two thirds of it start, partial outputs and their join, and 86 us on
+// 40960 (994 TFLOP/s; 1150 in steady state, where the scores' products, held by
 // shared memory at N = 64, take twice the outputs' time).
 //
 // Four warps bring in the K and V rows, a quarter of a tile each, through the
@@ -734,8 +734,7 @@ __global__ void __launch_bounds__(MassCfg<D>::kThreads, D == 256 ? 1 : 2) attn_m
 Maps make_maps(const AttnParams &p) {
   Maps maps = {};
   maps.box = p.page % 16 == 0 ? 16 : (p.page % 8 == 0 ? 8 : 0);
-  // Coordinates are 32-bit.
-  if ((long long)p.pages * p.Hkv > 0x7fffffffLL) maps.box = 0;
+  // Coordinates are 32-bit: the entry point refuses pages * H_kv from 2^31 on.
   if (maps.box && (!encode_rows(&maps.k, p.k, p.d, 1, p.page, p.pages * p.Hkv, maps.box) ||
                    !encode_rows(&maps.v, p.v, p.d, 1, p.page, p.pages * p.Hkv, maps.box)))
     maps.box = 0;
