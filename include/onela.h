@@ -248,7 +248,8 @@ ONELA_API int onela_decode_step(onela_handle *h, int32_t W_prev, int32_t W,
  * while the previous step finishes, as with ONELA_FLAG_PDL, but without its
  * contract across calls): only a step whose early record writes would replace
  * a depth stored before the call (possible past T_max steps, with folds) is an
- * ordinary launch.  The first step of a call is always an ordinary launch.
+ * ordinary launch.  The first step of a call is an ordinary launch too, unless
+ * ONELA_FLAG_PDL is set, whose contract then covers it.
  * Capacity: T + n <= T_max unless the handle has folded since the last
  * rewind.  q, k, v and o must start on 16-byte boundaries on a tensor-core
  * handle.  Every check that can be made on the host is made before the first
@@ -511,6 +512,8 @@ enum {
  *                     alone loses nothing.  o is summed before it is divided by
  *                     the sum of weights, each weight at most 2^8, so |v| times
  *                     2^8 times the tokens has to stay below 3e38.
+ *                     An infinite v that is attended to gives infinities or
+ *                     NaN in its columns.
  *   kernel            ONELA_KERNEL_AUTO; ONELA_KERNEL_SIMT (any shape) or
  *                     ONELA_KERNEL_TC (bf16, d in {64, 128, 256}, pools and q
  *                     rows on 16-byte boundaries, o on 4) to force one.
