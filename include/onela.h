@@ -470,7 +470,8 @@ ONELA_API int onela_decode_step_noalloc(const onela_config *cfg, int32_t t, int3
  *     at the same time (other streams, two captured graphs) need scratch of
  *     their own.
  *   - Outputs must not overlap inputs, or one another, except where a call
- *     says so.
+ *     says so.  (An output over lengths or a table, and what else could lead
+ *     a kernel astray, is refused: ONELA_ERR_ARG.)
  *   - `status` is a DEVICE int32 or NULL.  A call ORs ONELA_STATUS_* bits
  *     into it for what its device-side data got wrong; the caller clears it.
  *     Nothing out of range is read or written either way.

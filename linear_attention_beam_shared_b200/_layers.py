@@ -269,11 +269,11 @@ def onela_paged_attention_scratch_bytes(R, W, H_q, H_kv, d, dtype, page, pages, 
                                         q_stride=None):
     """Bytes of scratch a call of these sizes needs (to keep one buffer for all
     of a decode's calls); 0 for sizes no call takes.  q_stride: elements between
-    q's tokens (default: dense; of no account for a single one).  The kernels need different sizes: a bf16 call
-    whose q_stride is no multiple of 8, whose q or pools start off a 16-byte
-    boundary or whose o starts off a 4-byte one takes the general kernel.  The
-    stride is looked at here; for such addresses ask with
-    kernel=ONELA_KERNEL_SIMT, and for both with the larger of the two."""
+    q's tokens (default: dense; of no account for a single one).  The kernels
+    need different sizes: a bf16 call whose q_stride is no multiple of 8, whose q
+    or pools start off a 16-byte boundary or whose o starts off a 4-byte one
+    takes the general kernel.  The stride is looked at here; for such addresses
+    ask with kernel=ONELA_KERNEL_SIMT, and for both with the larger of the two."""
     if q_stride is None or R * W == 1:  # a single token is dense
         q_stride = H_q * d
     c = _filled(onela_attention_config, (R, W, H_q, H_kv, d, _CODE_OF[dtype], kernel, page, pages, row_pages, beam_page,

@@ -28,6 +28,21 @@ bool valid_dtype(int d) { return d == ONELA_F32 || d == ONELA_BF16; }
 size_t esize(int d) { return d == ONELA_BF16 ? 2 : 4; }
 bool aligned(const void *p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
+// Device memory a call reads or writes; empty where the pointer is null.
+struct Span {
+  uintptr_t at, bytes;
+  Span(const void *p, size_t n) : at(reinterpret_cast<uintptr_t>(p)), bytes(p ? n : 0) {}
+  bool overlaps(const Span &o) const { return bytes && o.bytes && at < o.at + o.bytes && o.at < at + bytes; }
+};
+// Is any of `a` over any of `b`?
+template <size_t N, size_t M>
+bool overlap(const Span (&a)[N], const Span (&b)[M]) {
+  for (const Span &x : a)
+    for (const Span &y : b)
+      if (x.overlaps(y)) return true;
+  return false;
+}
+
 // Switch to the call's device for its duration.
 struct DeviceGuard {
   int prev = -1;
@@ -143,6 +158,15 @@ int onela_paged_attention(const onela_attention_config *cfg, const void *q, cons
   const size_t need = onela::attention_scratch_bytes(c, mass_out != nullptr, p);
   if (need > 0 && (!scratch || !aligned(scratch, 256))) return ONELA_ERR_ARG;
   if (scratch_bytes < need) return ONELA_ERR_SCRATCH;
+  // Every warp derives its work from the lengths and the tables, and they have
+  // to find the same: nothing that is written may lie over them.
+  const size_t rows = (size_t)c.R * c.W * c.H_q, cells = (size_t)c.R * c.H_kv * c.page * c.row_pages;
+  const Span out[] = {{o, rows * c.d * es}, {lse, rows * 4}, {mass_out, cells * 4}, {scratch, need}, {status, 4}};
+  const Span plan[] = {{lengths, (size_t)c.R * 4},
+                       {table, (size_t)c.R * c.row_pages * 4},
+                       {beam_lengths, (size_t)c.R * c.W * 4},
+                       {beam_table, (size_t)c.R * c.W * c.beam_row_pages * 4}};
+  if (overlap(out, plan)) return ONELA_ERR_ARG;
   return on_device(c.device,
                    [&] { return onela::launch_attention(c, p, scratch, static_cast<cudaStream_t>(stream)); });
 }
@@ -217,6 +241,21 @@ int onela_cache_evict(const onela_cache_evict_config *cfg, const void *k_pool, c
     if (!aligned(scratch, 256)) return ONELA_ERR_ARG;
     if (scratch_bytes < onela_cache_evict_scratch_bytes(&c)) return ONELA_ERR_SCRATCH;
   }
+  // The CTAs of a cluster have to find the same lengths and weights each time
+  // they look, and the copy the positions that were found: nothing that is
+  // written may lie over them.
+  const size_t heads = (size_t)c.R * c.H_kv, slot = (size_t)c.H_kv * c.page * c.d * es;
+  const Span found[] = {{kept ? kept : scratch, heads * c.keep * 4}};
+  const Span out[] = {{dst_lengths, (size_t)c.R * 4},
+                      {dst_mass, heads * c.page * c.dst_row_pages * 4},
+                      {dst_k, (size_t)c.dst_pages * slot},
+                      {dst_v, (size_t)c.dst_pages * slot},
+                      {status, 4}};
+  const Span plan[] = {{lengths, (size_t)c.R * 4},
+                       {mass, heads * c.page * c.row_pages * 4},
+                       {table, (size_t)c.R * c.row_pages * 4},
+                       {dst_table, (size_t)c.R * c.dst_row_pages * 4}};
+  if (overlap(out, plan) || overlap(found, plan) || overlap(found, out)) return ONELA_ERR_ARG;
   onela::CacheEvictParams p = {};
   p.R = c.R;
   p.Hkv = c.H_kv;

@@ -223,3 +223,39 @@ def test_scratch_bytes_of_a_spaced_out_q():
     assert L.onela_paged_attention_scratch_bytes(*sizes, q_stride=8 * 64 - 1) == 0
     with pytest.raises(ValueError):
         L.onela_paged_attention_scratch_bytes(*sizes, q_stride=1 << 63)
+
+
+def apart(n, first=1 << 40, step=1 << 36):
+    """n addresses far from one another."""
+    return [first + i * step for i in range(n)]
+
+
+@pytest.mark.parametrize("out", ["o", "lse", "mass_out", "scratch"])
+@pytest.mark.parametrize("over", ["lengths", "table", "bl", "bt"])
+def test_attention_refuses_outputs_over_its_plan(out, over):
+    """An output that begins inside, or reaches into, the lengths or a table."""
+    import linear_attention_beam_shared_b200 as L
+    cfg = attention(L, beam_page=1, beam_pages=9, beam_row_pages=5)
+    names = ["q", "k", "v", "table", "lengths", "bk", "bv", "bt", "bl", "mass_out", "o", "lse", "scratch"]
+    good = dict(zip(names, apart(len(names))))
+    sizes = dict(o=2 * 3 * 8 * 64 * 2, lse=2 * 3 * 8 * 4, mass_out=2 * 2 * 640 * 4, scratch=256)
+    for at in (good[over], good[over] - sizes[out] + (256 if out == "scratch" else 4)):
+        a = dict(good, **{out: at})
+        if out == "scratch":
+            a["scratch"] -= a["scratch"] % 256
+        assert call_attention(L, cfg, **a) == L.ONELA_ERR_ARG
+
+
+@pytest.mark.parametrize("out,over", [(o, p) for o in ("dl", "dm", "dk", "dv", "kept", "scratch")
+                                      for p in ("lengths", "mass", "table", "dt")] +
+                         [("kept", p) for p in ("dl", "dm", "dk", "dv")] + [("scratch", p) for p in ("dl", "dm", "dk", "dv")])
+def test_evict_refuses_outputs_over_its_plan(out, over):
+    import linear_attention_beam_shared_b200 as L
+    cfg = evict_cfg(L)
+    names = ["k", "v", "table", "lengths", "mass", "dk", "dv", "dt", "dl", "dm", "kept", "scratch"]
+    good = dict(zip(names, apart(len(names))))
+    if out == "scratch":
+        good["kept"] = None
+    sizes = dict(dl=8, dm=2 * 2 * 32 * 4, dk=6 * 2 * 16 * 64 * 2, dv=6 * 2 * 16 * 64 * 2, kept=2 * 2 * 30 * 4, scratch=512)
+    for at in (good[over], good[over] + (0 if out == "scratch" else 4) - sizes[out] + (256 if out == "scratch" else 0)):
+        assert call_evict(L, cfg, **dict(good, **{out: at})) == L.ONELA_ERR_ARG
